@@ -31,6 +31,8 @@ FLAG_VALU_FOLD = 0x1
 FLAG_QUANTIZED_CKPT = 0x2
 FLAG_STAGGER_FLUSH = 0x4
 FLAG_MX_SCALE_CEIL = 0x8
+KVERR_NO_PAGES, KVERR_TOO_LONG, KVERR_BAD_SLOT, KVERR_CLAMPED = 0x1, 0x2, 0x4, 0x8
+ROT_HALVES, ROT_ADJACENT = 0, 1
 
 
 class ReplayConfig(ctypes.Structure):
@@ -50,8 +52,33 @@ class ReplayLayout(ctypes.Structure):
         (n, ctypes.c_uint64) for n in ("book_off", "book_bytes", "err_off")]
 
 
+class KVConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("abi_version", "batch", "npages", "page_size", "max_pages")]
+
+
+class KVLayer(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("abi_version", "io_dtype", "cache_dtype", "nheads", "nkv", "head_dim",
+                                              "npages", "page_size", "rot_dim", "rot_style")]
+
+
+class KVAppendArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v")] + [
+        (n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride")] + [
+        (n, ctypes.c_void_p) for n in ("slots", "pos", "freq", "axis")] + [
+        (n, ctypes.c_int32) for n in ("naxes", "rows")] + [
+        (n, ctypes.c_void_p) for n in ("q_out", "K", "V", "k_scale", "v_scale", "err")]
+
+
+class KVAttentionArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64)] + [
+        (n, ctypes.c_void_p) for n in ("K", "V", "k_scale", "v_scale", "table", "end", "active")] + [
+        (n, ctypes.c_int32) for n in ("batch", "max_pages", "ntok", "window")] + [("scale", ctypes.c_float)] + [
+        (n, ctypes.c_void_p) for n in ("o", "lse", "err")]
+
+
 _vp, _i32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
 _CP, _IP, _LP = ctypes.POINTER(ReplayConfig), ctypes.POINTER(ReplayInputs), ctypes.POINTER(ReplayLayout)
+_KC, _KL = ctypes.POINTER(KVConfig), ctypes.POINTER(KVLayer)
 
 _SIGS = {
     "replay_abi_version": ([], _i32),
@@ -98,6 +125,14 @@ _SIGS = {
     "replay_standin_linear": ([_vp, _vp, _vp, _i32, _i32, _i32, _vp], _i32),
     "replay_standin_attention": ([_vp, ctypes.c_int64, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, ctypes.c_float,
                                   _vp], _i32),
+    "replay_kv_bytes": ([_KC], _sz),
+    "replay_kv_reset": ([_KC, _vp, _vp], _i32),
+    "replay_kv_reserve": ([_KC, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _vp], _i32),
+    "replay_kv_commit": ([_KC, _vp, _vp, _vp], _i32),
+    "replay_kv_release": ([_KC, _vp, _vp, _vp], _i32),
+    "replay_kv_append": ([_KL, ctypes.POINTER(KVAppendArgs), _vp], _i32),
+    "replay_kv_attention_workspace": ([_KL, _i32, _i32], _sz),
+    "replay_kv_attention": ([_KL, ctypes.POINTER(KVAttentionArgs), _vp, _sz, _vp], _i32),
     "replay_stream_copy": ([_vp, _vp, _sz, _vp], _i32),
     "replay_stream_read": ([_vp, _sz, _vp, _vp], _i32),
 }
@@ -535,6 +570,258 @@ def standin_attention(q, K, V, scale, o=None):
     _check(_lib.replay_standin_attention(ctypes.c_void_p(q.data_ptr()), q.stride(0), _ptr(K, bf, "K"),
                                          _ptr(V, bf, "V"), _ptr(o, bf, "o"), B, Hq, Hkv, D, L, float(scale),
                                          _stream()), "replay_standin_attention")
+    return o
+
+
+# ---- paged key/value cache ---------------------------------------------------------
+def kv_config(batch, npages, page_size, max_pages) -> KVConfig:
+    return KVConfig(ABI_VERSION, batch, npages, page_size, max_pages)
+
+
+def kv_bytes(cfg: KVConfig) -> int:
+    return _lib.replay_kv_bytes(ctypes.byref(cfg))
+
+
+def kv_layer(nheads, nkv, head_dim, npages, page_size, io_dtype=BF16, cache_dtype=None, rot_dim=0,
+             rot_style=ROT_HALVES) -> KVLayer:
+    return KVLayer(ABI_VERSION, io_dtype, io_dtype if cache_dtype is None else cache_dtype, nheads, nkv, head_dim,
+                   npages, page_size, rot_dim, rot_style)
+
+
+def _kv_torch_dtypes(layer: KVLayer):
+    """(io dtype, cache dtype) of a layer as torch dtypes."""
+    torch = _torch()
+    kinds = {BF16: torch.bfloat16, F16: torch.float16, FP8_E4M3: torch.float8_e4m3fn}
+    return kinds.get(layer.io_dtype), kinds.get(layer.cache_dtype)
+
+
+def kv_cache(layer: KVLayer, device="cuda"):
+    """Zeroed K and V of one layer: [npages][Hkv][page_size][D] in its cache dtype."""
+    torch = _torch()
+    _, kind = _kv_torch_dtypes(layer)
+    shape = (layer.npages, layer.nkv, layer.page_size, layer.head_dim)
+    one = lambda: torch.zeros(shape, dtype=torch.uint8 if kind == torch.float8_e4m3fn else kind,  # noqa: E731
+                              device=device).view(kind)
+    return one(), one()
+
+
+class _On:
+    """Makes a tensor's device the current one for a call, so that the launch goes to that
+    device's current stream, and checks that the call's other tensors are on it too."""
+
+    def __init__(self, device):
+        torch = _torch()
+        if device.type != "cuda":
+            raise ValueError("the paged cache's tensors must be device tensors")
+        self.device = device
+        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def ptr(self, t, dtype=None, name="tensor", shape=None):
+        """Address of a contiguous tensor (None stays None)."""
+        if t is None:
+            return None
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, expected {self.device}")
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        return _ptr(t, dtype, name).value
+
+    def rows(self, t, dtype, name, rows, width):
+        """(address, row stride) of [rows][width] with contiguous rows."""
+        if t.dim() != 2 or tuple(t.shape) != (rows, width):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, width)}")
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, expected {self.device}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+        if width > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name} must have contiguous rows")
+        return t.data_ptr(), t.stride(0) if rows > 1 else width
+
+
+class KVPages:
+    """The page pool of a model's attention layers (replay_kv_* in the C ABI): block tables,
+    slot maps and free pages in one int32 device region `mem` (its own, reset, unless given)."""
+
+    def __init__(self, cfg: KVConfig, mem=None, device="cuda"):
+        torch = _torch()
+        self.cfg = cfg
+        words = kv_bytes(cfg) // 4
+        if words == 0:
+            raise ReplayError(ERR_SHAPE, "kv config")
+        self.mem = torch.empty(words, dtype=torch.int32, device=device) if mem is None else mem
+        if self.mem.dtype != torch.int32 or self.mem.dim() != 1 or self.mem.numel() < words:
+            raise ValueError(f"mem must be int32 with {words} words")
+        self.device = self.mem.device
+        if mem is None:
+            self.reset()
+
+    def _part(self, at, n):
+        return self.mem[at:at + n]
+
+    @property
+    def _bp(self):
+        return (self.cfg.batch + 63) // 64 * 64
+
+    @property
+    def nfree(self):
+        return self._part(0, 1)
+
+    @property
+    def err(self):
+        return self._part(1, 1)
+
+    @property
+    def len(self):
+        return self._part(64, self.cfg.batch)
+
+    @property
+    def end(self):
+        return self._part(64 + self._bp, self.cfg.batch)
+
+    @property
+    def held(self):
+        return self._part(64 + 2 * self._bp, self.cfg.batch)
+
+    @property
+    def table(self):
+        c = self.cfg
+        return self._part(64 + 7 * self._bp, c.batch * c.max_pages).view(c.batch, c.max_pages)
+
+    @property
+    def free(self):
+        return self._part(64 + 7 * self._bp + self.cfg.batch * self.cfg.max_pages, self.cfg.npages)
+
+    def reset(self):
+        with _On(self.device) as on:
+            _check(_lib.replay_kv_reset(ctypes.byref(self.cfg), on.ptr(self.mem), _stream()), "replay_kv_reset")
+
+    def reserve(self, ntok=1, counts=None, active=None, rows=None, slots=None, pos=None, starts=None):
+        """Pages for a step's new tokens: `ntok` each, rows [ntok][B], or `counts` (device int32 [B]),
+        packed rows (`rows` of them in all, or as many as `slots` has).  Returns (slots, pos), with
+        counts (slots, pos, starts)."""
+        torch = _torch()
+        B = self.cfg.batch
+        with _On(self.device) as on:
+            if slots is not None:
+                rows = slots.numel() if rows is None else rows
+            elif rows is None:
+                if counts is not None:
+                    raise ValueError("counts need rows (or slots): how many rows the step's arrays have")
+                rows = ntok * B
+            if slots is None:
+                slots = torch.empty(rows, dtype=torch.int64, device=self.device)
+            if pos is None:
+                pos = torch.empty(rows, dtype=torch.int32, device=self.device)
+            if counts is not None:
+                ntok = 0
+                if starts is None:
+                    starts = torch.empty(B + 1, dtype=torch.int32, device=self.device)
+            _check(_lib.replay_kv_reserve(
+                ctypes.byref(self.cfg), on.ptr(self.mem), int(ntok), on.ptr(counts, torch.int32, "counts", (B,)),
+                on.ptr(active, torch.uint8, "active", (B,)), int(rows), on.ptr(slots, torch.int64, "slots", (rows,)),
+                on.ptr(pos, torch.int32, "pos", (rows,)), on.ptr(starts, torch.int32, "starts", (B + 1,)), _stream()),
+                "replay_kv_reserve")
+        return (slots, pos) if counts is None else (slots, pos, starts)
+
+    def commit(self, accepted=None):
+        """Keeps accepted[b] (device int32 [B], None = all) of the open step's tokens."""
+        with _On(self.device) as on:
+            _check(_lib.replay_kv_commit(ctypes.byref(self.cfg), on.ptr(self.mem),
+                                         on.ptr(accepted, _torch().int32, "accepted", (self.cfg.batch,)), _stream()),
+                   "replay_kv_commit")
+
+    def release(self, mask=None):
+        """Empties the sequences `mask` (device uint8 [B], None = all) marks; their pages are free again."""
+        with _On(self.device) as on:
+            _check(_lib.replay_kv_release(ctypes.byref(self.cfg), on.ptr(self.mem),
+                                          on.ptr(mask, _torch().uint8, "mask", (self.cfg.batch,)), _stream()),
+                   "replay_kv_release")
+
+
+def kv_append(layer: KVLayer, K, V, k, v, slots, q=None, q_out=None, pos=None, freq=None, axis=None, k_scale=None,
+              v_scale=None, err=None):
+    """Rotates and caches a step's rows (replay_kv_append): k and v [rows][Hkv*D] and q [rows][Hq*D]
+    (any row stride) in the io dtype, slots int64 [rows], pos int32 [naxes][rows] (or [rows]),
+    freq fp32 [rot_dim/2], axis uint8 [rot_dim/2].  Returns q_out (None without q)."""
+    torch = _torch()
+    io, kind = _kv_torch_dtypes(layer)
+    n = k.shape[0]
+    shape = (layer.npages, layer.nkv, layer.page_size, layer.head_dim)
+    a = KVAppendArgs()
+    with _On(K.device) as on:
+        a.K, a.V = on.ptr(K, kind, "K", shape), on.ptr(V, kind, "V", shape)
+        a.rows = n
+        a.k, a.k_stride = on.rows(k, io, "k", n, layer.nkv * layer.head_dim)
+        a.v, a.v_stride = on.rows(v, io, "v", n, layer.nkv * layer.head_dim)
+        if q is not None:
+            a.q, a.q_stride = on.rows(q, io, "q", n, layer.nheads * layer.head_dim)
+            if q_out is None:
+                q_out = torch.zeros((n, layer.nheads * layer.head_dim), dtype=io, device=K.device)
+            a.q_out = on.ptr(q_out, io, "q_out", (n, layer.nheads * layer.head_dim))
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        a.slots = on.ptr(slots, torch.int64, "slots", (n,))
+        if layer.rot_dim > 0:
+            if pos is None or freq is None:
+                raise ValueError("a rotated layer needs pos and freq")
+            a.naxes = 1 if pos.dim() == 1 else pos.shape[0]
+            a.pos = on.ptr(pos, torch.int32, "pos", (n,) if pos.dim() == 1 else (a.naxes, n))
+            a.freq = on.ptr(freq, torch.float32, "freq", (layer.rot_dim // 2,))
+            a.axis = on.ptr(axis, torch.uint8, "axis", (layer.rot_dim // 2,))
+        a.k_scale = on.ptr(k_scale, torch.float32, "k_scale", (layer.nkv,))
+        a.v_scale = on.ptr(v_scale, torch.float32, "v_scale", (layer.nkv,))
+        a.err = on.ptr(err, torch.int32, "err", (1,))
+        _check(_lib.replay_kv_append(ctypes.byref(layer), ctypes.byref(a), _stream()), "replay_kv_append")
+    return q_out
+
+
+def kv_attention_workspace(layer: KVLayer, batch: int, ntok: int = 1) -> int:
+    return _lib.replay_kv_attention_workspace(ctypes.byref(layer), int(batch), int(ntok))
+
+
+def kv_attention(layer: KVLayer, q, K, V, table, end, ntok=1, scale=None, window=0, active=None, k_scale=None,
+                 v_scale=None, o=None, lse=None, err=None, ws=None):
+    """Attention of the last `ntok` tokens of every sequence over its pages (replay_kv_attention):
+    q [ntok*B][Hq*D] (any row stride), table int32 [B][max_pages], end int32 [B].  scale None is
+    D ** -0.5.  Returns o [ntok][B][Hq][D]; lse (fp32 [ntok][B][Hq]) is filled if given.  ws: a
+    uint8 tensor of kv_attention_workspace bytes; one is allocated for the call if None."""
+    torch = _torch()
+    io, kind = _kv_torch_dtypes(layer)
+    B = end.shape[0]
+    shape = (layer.npages, layer.nkv, layer.page_size, layer.head_dim)
+    a = KVAttentionArgs()
+    with _On(K.device) as on:
+        a.q, a.q_stride = on.rows(q, io, "q", ntok * B, layer.nheads * layer.head_dim)
+        a.K, a.V = on.ptr(K, kind, "K", shape), on.ptr(V, kind, "V", shape)
+        a.k_scale = on.ptr(k_scale, torch.float32, "k_scale", (layer.nkv,))
+        a.v_scale = on.ptr(v_scale, torch.float32, "v_scale", (layer.nkv,))
+        if table.dim() != 2:
+            raise ValueError("table must be [B][max_pages]")
+        a.table = on.ptr(table, torch.int32, "table", (B, table.shape[1]))
+        a.end = on.ptr(end, torch.int32, "end", (B,))
+        a.active = on.ptr(active, torch.uint8, "active", (B,))
+        a.batch, a.max_pages, a.ntok, a.window = B, table.shape[1], ntok, window
+        a.scale = layer.head_dim ** -0.5 if scale is None else scale
+        if o is None:
+            o = torch.zeros((ntok, B, layer.nheads, layer.head_dim), dtype=io, device=K.device)
+        a.o = on.ptr(o, io, "o", (ntok, B, layer.nheads, layer.head_dim))
+        a.lse = on.ptr(lse, torch.float32, "lse", (ntok, B, layer.nheads))
+        a.err = on.ptr(err, torch.int32, "err", (1,))
+        need = kv_attention_workspace(layer, B, ntok)
+        if ws is None:
+            ws = torch.empty(max(need, 1), dtype=torch.uint8, device=K.device)
+        _check(_lib.replay_kv_attention(ctypes.byref(layer), ctypes.byref(a), on.ptr(ws, torch.uint8, "ws"),
+                                        ws.numel(), _stream()), "replay_kv_attention")
     return o
 
 

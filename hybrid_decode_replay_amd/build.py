@@ -14,7 +14,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libreplayssm.so")
 SOURCES = ["host.cpp", "mamba2.hip", "mamba2_f16.hip", "mamba2_fp8.hip", "gdn.hip", "gdn_f16.hip", "gdn_fp8.hip",
-           "aux.hip", "conv.hip", "standin.hip"]
+           "aux.hip", "conv.hip", "standin.hip", "kv_pages.hip", "kv_append.hip", "kv_attention_bf16.hip",
+           "kv_attention_bf16_fp8.hip", "kv_attention_f16.hip", "kv_attention_f16_fp8.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

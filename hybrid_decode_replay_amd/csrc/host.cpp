@@ -11,6 +11,28 @@
 #include <vector>
 
 #include "internal.hpp"
+#include "kv.hpp"
+
+namespace rs {
+
+// Rows that share a key/value head fill 16-row products; a wave takes one or two such blocks, and
+// past 32 rows the waves of a workgroup take different rows over the same tokens, so that the
+// cache is still read once.  Wide heads keep to one block a wave (two would leave one wave per
+// SIMD).  More rows than a workgroup holds make further chunks, which read the cache again.
+KvPlan kv_attention_plan(int D, bool fp8, int rows)
+{
+    KvPlan p;
+    p.RB = D == 256 || rows <= 16 ? 1 : 2;
+    const int groups = (rows + 16 * p.RB - 1) / (16 * p.RB);
+    p.RW = groups <= 1 ? 1 : (groups == 2 ? 2 : 4);
+    const int most = 16 * p.RB * p.RW;
+    p.rpc = rows < most ? rows : most;
+    p.nchunk = (rows + most - 1) / most;
+    p.nwg = 256 * kv_occ(D, fp8, p.RB);
+    return p;
+}
+
+}  // namespace rs
 
 struct replay_state {
     replay_config cfg;
@@ -184,6 +206,123 @@ replay_status check_ptr(const void* p, const char* name)
 {
     if (!p) return fail(REPLAY_ERR_ARG, "%s is NULL", name);
     if (!aligned(p, 16)) return fail(REPLAY_ERR_ALIGN, "%s is not 16-byte aligned", name);
+    return REPLAY_OK;
+}
+
+// ---- paged key/value cache ----
+bool page_size_ok(int32_t n) { return n == 16 || n == 32 || n == 64 || n == 128 || n == 256; }
+
+int log2_of(int32_t n)
+{
+    int k = 0;
+    while ((1 << k) < n) ++k;
+    return k;
+}
+
+// Limits a table has to keep so that positions, units of work and page indices stay in 32 bits.
+replay_status check_kv_table(int32_t batch, int32_t max_pages, int32_t page_size)
+{
+    if (batch < 1 || batch > 4096) return fail(REPLAY_ERR_SHAPE, "batch %d outside [1, 4096]", batch);
+    if (max_pages < 1 || (long long)max_pages * page_size >= (1LL << 30) || (long long)batch * max_pages >= (1LL << 30))
+        return fail(REPLAY_ERR_SHAPE, "max_pages %d: need >= 1, max_pages * page_size and batch * max_pages below 2^30",
+                    max_pages);
+    return REPLAY_OK;
+}
+
+replay_status check_kv_config(const replay_kv_config* c)
+{
+    if (!c) return fail(REPLAY_ERR_ARG, "kv config is NULL");
+    if (c->abi_version != REPLAY_ABI_VERSION)
+        return fail(REPLAY_ERR_ARG, "abi_version %d, library implements %d", c->abi_version, REPLAY_ABI_VERSION);
+    if (!page_size_ok(c->page_size))
+        return fail(REPLAY_ERR_SHAPE, "page_size %d must be 16, 32, 64, 128 or 256", c->page_size);
+    if (c->npages < 1) return fail(REPLAY_ERR_SHAPE, "npages must be >= 1");
+    return check_kv_table(c->batch, c->max_pages, c->page_size);
+}
+
+uint64_t kv_words(const replay_kv_config* c)
+{
+    const uint64_t bp = ((uint64_t)c->batch + 63) / 64 * 64;
+    return 64 + 7 * bp + (uint64_t)c->batch * c->max_pages + (uint64_t)c->npages;
+}
+
+replay_status kv_pool(const replay_kv_config* c, void* mem, rs::KvPool* p)
+{
+    replay_status s = check_kv_config(c);
+    if (s != REPLAY_OK) return s;
+    if (!mem) return fail(REPLAY_ERR_ARG, "mem is NULL");
+    if (!aligned(mem, 256)) return fail(REPLAY_ERR_ALIGN, "mem is not 256-byte aligned");
+    const int bp = (c->batch + 63) / 64 * 64;
+    int32_t* w = static_cast<int32_t*>(mem);
+    *p = rs::KvPool{c->batch, c->npages, log2_of(c->page_size), c->max_pages, w, w + 64, w + 64 + bp, w + 64 + 2 * bp,
+                    w + 64 + 3 * bp, w + 64 + 7 * bp, w + 64 + 7 * bp + (size_t)c->batch * c->max_pages, bp};
+    return REPLAY_OK;
+}
+
+replay_status check_kv_layer(const replay_kv_layer* l)
+{
+    if (!l) return fail(REPLAY_ERR_ARG, "kv layer is NULL");
+    if (l->abi_version != REPLAY_ABI_VERSION)
+        return fail(REPLAY_ERR_ARG, "abi_version %d, library implements %d", l->abi_version, REPLAY_ABI_VERSION);
+    if (l->io_dtype != REPLAY_BF16 && l->io_dtype != REPLAY_F16)
+        return fail(REPLAY_ERR_DTYPE, "a paged cache's io_dtype must be REPLAY_BF16 or REPLAY_F16");
+    if (l->cache_dtype != l->io_dtype && l->cache_dtype != REPLAY_FP8_E4M3)
+        return fail(REPLAY_ERR_DTYPE, "cache_dtype must be io_dtype or REPLAY_FP8_E4M3");
+    if (l->nkv < 1 || l->nheads < l->nkv || l->nheads % l->nkv != 0 || l->nheads > 4096)
+        return fail(REPLAY_ERR_SHAPE, "nheads %d must be a multiple of nkv %d, at most 4096", l->nheads, l->nkv);
+    if (l->head_dim != 64 && l->head_dim != 128 && l->head_dim != 256)
+        return fail(REPLAY_ERR_UNSUPPORTED, "head dimension %d (64, 128 and 256 are built)", l->head_dim);
+    if (!page_size_ok(l->page_size))
+        return fail(REPLAY_ERR_SHAPE, "page_size %d must be 16, 32, 64, 128 or 256", l->page_size);
+    if (l->npages < 1) return fail(REPLAY_ERR_SHAPE, "npages must be >= 1");
+    if (l->rot_dim < 0 || l->rot_dim > l->head_dim || l->rot_dim % 16 != 0)
+        return fail(REPLAY_ERR_SHAPE, "rot_dim %d must be a multiple of 16 in [0, head_dim]", l->rot_dim);
+    if (l->rot_style != REPLAY_ROT_HALVES && l->rot_style != REPLAY_ROT_ADJACENT)
+        return fail(REPLAY_ERR_ARG, "unknown rot_style %d", l->rot_style);
+    return REPLAY_OK;
+}
+
+// Aligned as the elements of a small array are (per-sequence and per-row words may be slices).
+replay_status check_words(const void* p, const char* name, uintptr_t size)
+{
+    if (!p) return fail(REPLAY_ERR_ARG, "%s is NULL", name);
+    if (!aligned(p, size)) return fail(REPLAY_ERR_ALIGN, "%s is not %d-byte aligned", name, (int)size);
+    return REPLAY_OK;
+}
+
+replay_status check_kv_scales(const replay_kv_layer* l, const float* k, const float* v)
+{
+    const bool fp8 = l->cache_dtype == REPLAY_FP8_E4M3;
+    if (!fp8 && (k || v)) return fail(REPLAY_ERR_ARG, "k_scale and v_scale belong to an FP8 cache");
+    replay_status s;
+    if (fp8 && (s = check_words(k, "k_scale", 4)) != REPLAY_OK) return s;
+    if (fp8 && (s = check_words(v, "v_scale", 4)) != REPLAY_OK) return s;
+    return REPLAY_OK;
+}
+
+replay_status check_row_stride(int64_t stride, long long width, const char* name)
+{
+    if (stride < width || stride % 8 != 0 || stride >= (1LL << 31))
+        return fail(REPLAY_ERR_ARG, "%s %lld must be >= %lld, a multiple of 8 and below 2^31", name, (long long)stride,
+                    width);
+    return REPLAY_OK;
+}
+
+uint64_t kv_meta_bytes(const rs::KvPlan& p) { return align256((uint64_t)p.nwg * 16); }
+uint64_t kv_ml_bytes(const rs::KvPlan& p) { return align256((uint64_t)p.nwg * 2 * p.rpc * 8); }
+uint64_t kv_ws_bytes(const rs::KvPlan& p, int D)
+{
+    return kv_meta_bytes(p) + kv_ml_bytes(p) + align256((uint64_t)p.nwg * 2 * p.rpc * D * 4);
+}
+
+// Sizes of an attention call, and how it is cut.
+replay_status check_kv_call(const replay_kv_layer* l, int32_t batch, int32_t ntok, rs::KvPlan* plan)
+{
+    replay_status s = check_kv_layer(l);
+    if (s != REPLAY_OK) return s;
+    if (batch < 1 || batch > 4096) return fail(REPLAY_ERR_SHAPE, "batch %d outside [1, 4096]", batch);
+    if (ntok < 1 || ntok > REPLAY_MAX_BUF) return fail(REPLAY_ERR_CAPACITY, "ntok = %d outside [1, %d]", ntok, REPLAY_MAX_BUF);
+    *plan = rs::kv_attention_plan(l->head_dim, l->cache_dtype == REPLAY_FP8_E4M3, ntok * (l->nheads / l->nkv));
     return REPLAY_OK;
 }
 
@@ -1063,6 +1202,171 @@ replay_status replay_standin_attention(const void* q, int64_t q_stride, const vo
     return LAUNCH(rs::launch_standin_attention(q, K, V, o, B, Hq, Hkv, D, L, (size_t)q_stride, scale,
                                                (hipStream_t)stream),
                   "stand-in attention");
+}
+
+// ---- paged key/value cache ---------------------------------------------------
+size_t replay_kv_bytes(const replay_kv_config* cfg)
+{
+    if (check_kv_config(cfg) != REPLAY_OK) return 0;
+    (void)ok();
+    return (size_t)(kv_words(cfg) * 4);
+}
+
+replay_status replay_kv_reset(const replay_kv_config* cfg, void* mem, void* stream)
+{
+    rs::KvPool p;
+    const replay_status s = kv_pool(cfg, mem, &p);
+    if (s != REPLAY_OK) return s;
+    return LAUNCH(rs::launch_kv_reset(p, (hipStream_t)stream), "page pool reset");
+}
+
+replay_status replay_kv_reserve(const replay_kv_config* cfg, void* mem, int32_t ntok, const int32_t* counts,
+                                const uint8_t* active, int32_t rows, int64_t* slots, int32_t* pos, int32_t* starts,
+                                void* stream)
+{
+    rs::KvPool p;
+    replay_status s = kv_pool(cfg, mem, &p);
+    if (s != REPLAY_OK) return s;
+    if ((s = check_words(slots, "slots", 8)) != REPLAY_OK) return s;
+    if ((s = check_words(pos, "pos", 4)) != REPLAY_OK) return s;
+    if (counts) {
+        if ((s = check_words(counts, "counts", 4)) != REPLAY_OK) return s;
+        if ((s = check_words(starts, "starts", 4)) != REPLAY_OK) return s;
+        if (ntok != 0) return fail(REPLAY_ERR_ARG, "ntok must be 0 with counts");
+        if (rows < 1) return fail(REPLAY_ERR_SHAPE, "rows must be >= 1");
+    } else {
+        if (starts) return fail(REPLAY_ERR_ARG, "starts belongs to counts");
+        if (ntok < 1 || ntok > REPLAY_MAX_BUF)
+            return fail(REPLAY_ERR_CAPACITY, "ntok = %d outside [1, %d]", ntok, REPLAY_MAX_BUF);
+        if (rows < ntok * cfg->batch) return fail(REPLAY_ERR_SHAPE, "rows %d below ntok * batch", rows);
+    }
+    return LAUNCH(rs::launch_kv_reserve(p, ntok, counts, active, rows, slots, pos, starts, (hipStream_t)stream),
+                  "page reserve");
+}
+
+replay_status replay_kv_commit(const replay_kv_config* cfg, void* mem, const int32_t* accepted, void* stream)
+{
+    rs::KvPool p;
+    replay_status s = kv_pool(cfg, mem, &p);
+    if (s != REPLAY_OK) return s;
+    if (accepted && (s = check_words(accepted, "accepted", 4)) != REPLAY_OK) return s;
+    return LAUNCH(rs::launch_kv_commit(p, accepted, (hipStream_t)stream), "page commit");
+}
+
+replay_status replay_kv_release(const replay_kv_config* cfg, void* mem, const uint8_t* mask, void* stream)
+{
+    rs::KvPool p;
+    const replay_status s = kv_pool(cfg, mem, &p);
+    if (s != REPLAY_OK) return s;
+    return LAUNCH(rs::launch_kv_release(p, mask, (hipStream_t)stream), "page release");
+}
+
+replay_status replay_kv_append(const replay_kv_layer* layer, const replay_kv_append_args* args, void* stream)
+{
+    replay_status s = check_kv_layer(layer);
+    if (s != REPLAY_OK) return s;
+    if (!args) return fail(REPLAY_ERR_ARG, "append arguments are NULL");
+    const replay_kv_append_args& x = *args;
+    const int Hq = layer->nheads, Hkv = layer->nkv, D = layer->head_dim;
+    if (x.rows < 0 || x.rows > (1 << 25)) return fail(REPLAY_ERR_SHAPE, "rows %d outside [0, 2^25]", x.rows);
+    if ((s = check_ptr(x.K, "K")) != REPLAY_OK) return s;
+    if ((s = check_ptr(x.V, "V")) != REPLAY_OK) return s;
+    if ((s = check_kv_scales(layer, x.k_scale, x.v_scale)) != REPLAY_OK) return s;
+    if (!x.q != !x.q_out) return fail(REPLAY_ERR_ARG, "q and q_out go together");
+    if (x.err && !aligned(x.err, 4)) return fail(REPLAY_ERR_ALIGN, "err is not 4-byte aligned");
+    if (x.rows == 0) return ok();
+    if ((s = check_ptr(x.k, "k")) != REPLAY_OK) return s;
+    if ((s = check_ptr(x.v, "v")) != REPLAY_OK) return s;
+    if ((s = check_row_stride(x.k_stride, (long long)Hkv * D, "k_stride")) != REPLAY_OK) return s;
+    if ((s = check_row_stride(x.v_stride, (long long)Hkv * D, "v_stride")) != REPLAY_OK) return s;
+    if (x.q) {
+        if ((s = check_ptr(x.q, "q")) != REPLAY_OK) return s;
+        if ((s = check_ptr(x.q_out, "q_out")) != REPLAY_OK) return s;
+        if ((s = check_row_stride(x.q_stride, (long long)Hq * D, "q_stride")) != REPLAY_OK) return s;
+    }
+    if ((s = check_words(x.slots, "slots", 8)) != REPLAY_OK) return s;
+    if (layer->rot_dim > 0) {
+        if ((s = check_words(x.pos, "pos", 4)) != REPLAY_OK) return s;
+        if ((s = check_words(x.freq, "freq", 4)) != REPLAY_OK) return s;
+        if (x.naxes < 1 || x.naxes > 8) return fail(REPLAY_ERR_SHAPE, "naxes %d outside [1, 8]", x.naxes);
+    }
+    const rs::KvAppend a{x.q, x.k, x.v, x.q_stride, x.k_stride, x.v_stride, x.slots, x.pos, x.freq, x.axis, x.q_out,
+                         x.K, x.V, x.k_scale, x.v_scale, x.err, x.naxes, x.rows, Hq, Hkv, D, log2_of(layer->page_size),
+                         layer->rot_dim, (int64_t)layer->npages * layer->page_size};
+    return LAUNCH(rs::launch_kv_append(a, layer->io_dtype == REPLAY_BF16 ? rs::KV_BF16 : rs::KV_F16,
+                                       layer->cache_dtype == REPLAY_FP8_E4M3, layer->rot_style, (hipStream_t)stream),
+                  "cache append");
+}
+
+size_t replay_kv_attention_workspace(const replay_kv_layer* layer, int32_t batch, int32_t ntok)
+{
+    rs::KvPlan p;
+    if (check_kv_call(layer, batch, ntok, &p) != REPLAY_OK) return 0;
+    (void)ok();
+    return (size_t)kv_ws_bytes(p, layer->head_dim);
+}
+
+replay_status replay_kv_attention(const replay_kv_layer* layer, const replay_kv_attention_args* args, void* ws,
+                                  size_t ws_bytes, void* stream)
+{
+    if (!args) return fail(REPLAY_ERR_ARG, "attention arguments are NULL");
+    const replay_kv_attention_args& x = *args;
+    rs::KvPlan p;
+    replay_status s = check_kv_call(layer, x.batch, x.ntok, &p);
+    if (s != REPLAY_OK) return s;
+    const int Hq = layer->nheads, Hkv = layer->nkv, D = layer->head_dim;
+    if ((s = check_kv_table(x.batch, x.max_pages, layer->page_size)) != REPLAY_OK) return s;
+    if ((s = check_ptr(x.q, "q")) != REPLAY_OK) return s;
+    if ((s = check_row_stride(x.q_stride, (long long)Hq * D, "q_stride")) != REPLAY_OK) return s;
+    if ((s = check_ptr(x.K, "K")) != REPLAY_OK) return s;
+    if ((s = check_ptr(x.V, "V")) != REPLAY_OK) return s;
+    if ((s = check_ptr(x.o, "o")) != REPLAY_OK) return s;
+    if ((s = check_kv_scales(layer, x.k_scale, x.v_scale)) != REPLAY_OK) return s;
+    if ((s = check_words(x.table, "table", 4)) != REPLAY_OK) return s;
+    if ((s = check_words(x.end, "end", 4)) != REPLAY_OK) return s;
+    if (x.lse && !aligned(x.lse, 4)) return fail(REPLAY_ERR_ALIGN, "lse is not 4-byte aligned");
+    if (x.err && !aligned(x.err, 4)) return fail(REPLAY_ERR_ALIGN, "err is not 4-byte aligned");
+    if (x.window < 0) return fail(REPLAY_ERR_ARG, "window %d is negative", x.window);
+    if ((long long)x.batch * Hkv * p.nchunk * (((long long)x.max_pages * layer->page_size + 127) / 128 + 1) >= (1LL << 31))
+        return fail(REPLAY_ERR_SHAPE, "batch * nkv * max_pages * page_size too large");
+    if (!ws) return fail(REPLAY_ERR_ARG, "workspace is NULL");
+    if (!aligned(ws, 256) || ws_bytes < kv_ws_bytes(p, D))
+        return fail(REPLAY_ERR_ALIGN, "workspace needs %llu bytes, 256-byte aligned", (unsigned long long)kv_ws_bytes(p, D));
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    rs::KvAttention a;
+    a.q = x.q;
+    a.q_stride = x.q_stride;
+    a.K = x.K;
+    a.V = x.V;
+    a.k_scale = x.k_scale;
+    a.v_scale = x.v_scale;
+    a.table = x.table;
+    a.end = x.end;
+    a.active = x.active;
+    a.o = x.o;
+    a.lse = x.lse;
+    a.err = x.err;
+    a.meta = reinterpret_cast<int32_t*>(w);
+    a.part_ml = reinterpret_cast<float*>(w + kv_meta_bytes(p));
+    a.part_o = reinterpret_cast<float*>(w + kv_meta_bytes(p) + kv_ml_bytes(p));
+    a.B = x.batch;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.group = Hq / Hkv;
+    a.T = x.ntok;
+    a.npages = layer->npages;
+    a.page_shift = log2_of(layer->page_size);
+    a.max_pages = x.max_pages;
+    // a window past every position is none
+    a.window = x.window < x.max_pages * layer->page_size ? x.window : 0;
+    a.rows = x.ntok * a.group;
+    a.rpc = p.rpc;
+    a.nchunk = p.nchunk;
+    a.scale_log2 = (float)((double)x.scale * 1.4426950408889634);
+    const bool bf = layer->io_dtype == REPLAY_BF16, fp8 = layer->cache_dtype == REPLAY_FP8_E4M3;
+    const auto run = bf ? (fp8 ? rs::launch_kv_attention_bf16_fp8 : rs::launch_kv_attention_bf16)
+                        : (fp8 ? rs::launch_kv_attention_f16_fp8 : rs::launch_kv_attention_f16);
+    return LAUNCH(run(a, p, D, (hipStream_t)stream), "paged attention");
 }
 
 replay_status replay_stream_copy(void* dst, const void* src, size_t bytes, void* stream)

@@ -394,6 +394,162 @@ replay_status replay_standin_attention(const void *q, int64_t q_stride, const vo
                                        int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t L, float scale,
                                        void *stream);
 
+/* ---- paged key/value cache of the attention layers -------------------------
+ * A hybrid model's attention layers ([TR] "NVIDIA ve Dao AI Lab ...", section
+ * "ReplaySSM nasil calisir?": SSM layers interleaved with attention layers)
+ * keep the keys and values of every token.  Here they live in pages of
+ * page_size tokens taken from one pool, so that the cache follows the same
+ * batch slots, masked steps, arrivals and draft rounds as the replayed states:
+ *
+ *   replay_kv_reserve   pages and slots for a step's new tokens
+ *   replay_kv_append    (per layer) rotates q and k, writes k and v into them
+ *   replay_kv_attention (per layer) attention of the new tokens over the cache
+ *   replay_kv_commit    keeps the accepted ones
+ *   replay_kv_release   gives a departed sequence's pages back
+ *
+ * One pool serves every attention layer of a model; each layer has its own K
+ * and V, [npages][Hkv][page_size][D] in cache_dtype (values of a token's head
+ * contiguous).  Token i of sequence b is in page table[b][i / page_size] at
+ * offset i % page_size; its slot is page * page_size + offset.
+ *
+ * The pool's state is one caller-owned device region of int32 words
+ * (replay_kv_bytes; Bp = B rounded up to a multiple of 64):
+ *   word 0           number of free pages          word 1  error bits
+ *   64               len  [Bp]  tokens kept
+ *   64 + Bp          end  [Bp]  len plus the open step's tokens
+ *   64 + 2 Bp        held [Bp]  pages held
+ *   64 + 3 Bp        scratch [4 Bp]
+ *   64 + 7 Bp        table [B][max_pages], -1 where no page is held
+ *   then             stack of free pages [npages], the next one at the top
+ * All of it changes on the device only, in stream order, so a captured graph
+ * of a decode step can cross page boundaries.  Results depend on the calls made
+ * and their arguments alone (no atomics decide an order). */
+typedef struct {
+    int32_t abi_version;  /* REPLAY_ABI_VERSION                                    */
+    int32_t batch;        /* B in [1, 4096]                                        */
+    int32_t npages;       /* pages of the pool, >= 1                               */
+    int32_t page_size;    /* tokens per page: 16, 32, 64, 128 or 256               */
+    int32_t max_pages;    /* pages a sequence may hold; max_pages * page_size < 2^30,
+                             batch * max_pages < 2^30                              */
+} replay_kv_config;
+
+/* Error bits of the pool (sticky; cleared by replay_kv_reset). */
+#define REPLAY_KVERR_NO_PAGES 0x1u   /* reserve: the free pages did not suffice      */
+#define REPLAY_KVERR_TOO_LONG 0x2u   /* reserve: more tokens than max_pages hold, a negative
+                                        count, or rows past the arrays               */
+#define REPLAY_KVERR_BAD_SLOT 0x4u   /* append: a slot outside the cache (row skipped);
+                                        attention: a page outside it, or an `end` past the
+                                        table (those positions are masked)           */
+#define REPLAY_KVERR_CLAMPED  0x8u   /* commit: a count outside [0, end - len]       */
+
+/* Bytes of the pool's region (0 if the configuration is invalid).  The region
+ * must be 256-byte aligned. */
+size_t replay_kv_bytes(const replay_kv_config *cfg);
+/* Every page free (page 0 is handed out first), every sequence empty. */
+replay_status replay_kv_reset(const replay_kv_config *cfg, void *mem, void *stream);
+/* Opens a step: pages for n_b new tokens after each sequence's len, their slots
+ * and their positions.  Sequence b is served if its tokens fit (see
+ * REPLAY_KVERR_TOO_LONG) and the pages that all sequences up to b still need
+ * do not exceed the free ones; a sequence that needs no page is always served.
+ * It then takes its pages from the top of the stack, in order of b, and end[b]
+ * = len[b] + n_b; else end[b] = len[b], nothing is taken and an error bit is set.
+ *   counts == NULL: n_b = ntok (1..16) for every sequence (active, device uint8
+ *     [B] or NULL: for those with a nonzero byte, 0 for the others).  Token i of
+ *     sequence b has row i * B + b, as the step's inputs have; rows >= ntok * B.
+ *   counts (device int32 [B]): n_b = counts[b], 0 where inactive.  Rows are
+ *     packed, token i of sequence b at starts[b] + i, where starts (device int32
+ *     [B + 1]) receives the exclusive sums of all n_b and, last, their total
+ *     (sums are held at 2^31 - 1).  ntok must be 0.
+ * slots (device int64 [rows]) and pos (device int32 [rows]) receive every row's
+ * slot and position, -1 for the rows of a sequence that was not served and for
+ * rows without a token.  A second reserve before a commit opens the step anew;
+ * pages already held are kept. */
+replay_status replay_kv_reserve(const replay_kv_config *cfg, void *mem, int32_t ntok, const int32_t *counts,
+                                const uint8_t *active, int32_t rows, int64_t *slots, int32_t *pos, int32_t *starts,
+                                void *stream);
+/* Closes a step: len[b] += clamp(accepted[b], 0, end[b] - len[b]) (accepted:
+ * device int32 [B], NULL = all of them) and end[b] = len[b].  Pages of tokens
+ * that were not accepted stay held for the next step. */
+replay_status replay_kv_commit(const replay_kv_config *cfg, void *mem, const int32_t *accepted, void *stream);
+/* Empties the sequences whose mask[b] (device uint8 [B], NULL = all) is
+ * nonzero: their pages go back on the stack, len = end = held = 0.  A release
+ * right after a reserve that found them empty restores the stack. */
+replay_status replay_kv_release(const replay_kv_config *cfg, void *mem, const uint8_t *mask, void *stream);
+
+#define REPLAY_ROT_HALVES 0     /* pair p of a head: channels p and p + rot_dim / 2 */
+#define REPLAY_ROT_ADJACENT 1   /* pair p of a head: channels 2 p and 2 p + 1       */
+
+/* An attention layer over a paged cache. */
+typedef struct {
+    int32_t abi_version;  /* REPLAY_ABI_VERSION                                    */
+    int32_t io_dtype;     /* REPLAY_BF16 | REPLAY_F16: q, k, v and outputs         */
+    int32_t cache_dtype;  /* io_dtype, or REPLAY_FP8_E4M3 with a scale per head    */
+    int32_t nheads;       /* Hq query heads, a multiple of nkv                     */
+    int32_t nkv;          /* Hkv key/value heads; head h reads h / (Hq / Hkv)      */
+    int32_t head_dim;     /* D: 64, 128 or 256                                     */
+    int32_t npages, page_size;   /* as the pool's                                  */
+    int32_t rot_dim;      /* rotated channels of a head: a multiple of 16 up to D, 0 = none */
+    int32_t rot_style;    /* REPLAY_ROT_*                                          */
+} replay_kv_layer;
+
+/* Rows of a step on their way into the cache.  Row r of q, k and v starts at
+ * its pointer + r * its stride (elements, a multiple of 8; so q, k and v may be
+ * parts of one fused projection's rows).  All pointers are device pointers. */
+typedef struct {
+    const void *q, *k, *v;        /* [rows] of Hq*D (q may be NULL), Hkv*D, Hkv*D values, io_dtype */
+    int64_t q_stride, k_stride, v_stride;
+    const int64_t *slots;         /* [rows]; a negative slot skips the row          */
+    const int32_t *pos;           /* [naxes][rows] positions (rot_dim > 0 only)     */
+    const float *freq;            /* [rot_dim / 2] radians per position             */
+    const uint8_t *axis;          /* [rot_dim / 2] axis of each pair, NULL = 0; a pair whose
+                                     axis is >= naxes turns by 0                    */
+    int32_t naxes;                /* 1..8                                           */
+    int32_t rows;                 /* >= 0                                           */
+    void *q_out;                  /* [rows][Hq*D] io_dtype; with q only             */
+    void *K, *V;                  /* the layer's cache                              */
+    const float *k_scale, *v_scale;   /* [Hkv], FP8 cache only                      */
+    uint32_t *err;                /* error word (the pool's word 1) or NULL         */
+} replay_kv_append_args;
+
+/* Rotates q and k by their positions, writes q to q_out and k and v to their
+ * slots; skipped rows leave q_out as it was.  Pair p of a row turns by the angle
+ * pos[axis[p]][row] * freq[p], formed in 64 bits (a far position loses nothing):
+ *   x_i' = x_i cos - x_j sin,  x_j' = x_j cos + x_i sin  in fp32, rounded once.
+ * FP8: the code of x / scale of the head, round to nearest even, magnitudes past
+ * 448 saturated, NaN 0x7f.  No two rows may name the same slot. */
+replay_status replay_kv_append(const replay_kv_layer *layer, const replay_kv_append_args *args, void *stream);
+
+typedef struct {
+    const void *q;                /* [ntok * B] rows of Hq*D values, row t * B + b  */
+    int64_t q_stride;             /* elements between rows, a multiple of 8         */
+    const void *K, *V;
+    const float *k_scale, *v_scale;   /* [Hkv], FP8 cache only                      */
+    const int32_t *table;         /* [B][max_pages]                                 */
+    const int32_t *end;           /* [B] tokens in the cache, the ntok new ones last */
+    const uint8_t *active;        /* [B] or NULL: outputs of the others are left as they were */
+    int32_t batch, max_pages;     /* limits as replay_kv_config's                   */
+    int32_t ntok;                 /* T in [1, 16]                                   */
+    int32_t window;               /* positions a token sees, itself included; 0 = all */
+    float scale;                  /* of the scores                                  */
+    void *o;                      /* [T][B][Hq][D] io_dtype                         */
+    float *lse;                   /* [T][B][Hq] natural log of the sum of exponentials, or NULL */
+    uint32_t *err;                /* error word (the pool's word 1) or NULL         */
+} replay_kv_attention_args;
+
+/* Bytes of workspace (256-byte aligned) a call needs; 0 if its sizes are
+ * invalid.  It depends on the layer, batch and ntok, and holds nothing between
+ * calls; calls that may run at the same time need one each. */
+size_t replay_kv_attention_workspace(const replay_kv_layer *layer, int32_t batch, int32_t ntok);
+/* Attention of the last ntok tokens of every sequence over its cache: token t
+ * of sequence b is at position p = end[b] - ntok + t and, for head h,
+ *   o = sum_j w_j V_j,  w = softmax of scale * q.K_j  over max(0, p - window + 1) <= j <= p.
+ * A token that sees nothing (p < 0, or only positions without a page) gives
+ * o = 0 and lse = -inf.  What lies in masked positions does not matter, NaN
+ * included.  Softmax statistics and sums are fp32; weights are carried in two
+ * io_dtype terms. */
+replay_status replay_kv_attention(const replay_kv_layer *layer, const replay_kv_attention_args *args, void *ws,
+                                  size_t ws_bytes, void *stream);
+
 /* ---- measurement helpers ------------------------------------------------ */
 /* Streaming copy of `bytes` (multiple of 16) from src to dst: the in-run
  * bandwidth ceiling and the reference for hardware byte counters. */
