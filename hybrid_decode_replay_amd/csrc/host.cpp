@@ -308,7 +308,7 @@ replay_status check_row_stride(int64_t stride, long long width, const char* name
     return REPLAY_OK;
 }
 
-uint64_t kv_meta_bytes(const rs::KvPlan& p) { return align256((uint64_t)p.nwg * 16); }
+uint64_t kv_meta_bytes(const rs::KvPlan& p) { return align256((uint64_t)p.nwg * 8); }
 uint64_t kv_ml_bytes(const rs::KvPlan& p) { return align256((uint64_t)p.nwg * 2 * p.rpc * 8); }
 uint64_t kv_ws_bytes(const rs::KvPlan& p, int D)
 {

@@ -50,7 +50,8 @@ struct KvAttention {
     void* o;
     float* lse;
     uint32_t* err;
-    int32_t* meta;           // [nwg][4]: the split range each workgroup opens (combine's work)
+    int32_t* meta;           // [nwg][2]: the split ranges, by range (first and last workgroup) where there are no
+                             // more ranges than workgroups, else by the workgroup that opens one (range, last)
     float* part_ml;          // [2 nwg][rpc][2]: reference exponent and sum of each partial row
     float* part_o;           // [2 nwg][rpc][D]
     int B, Hq, Hkv, group, T, npages, page_shift, max_pages, window;
@@ -64,10 +65,12 @@ struct KvAttention {
 struct KvPlan {
     int RB, RW, rpc, nchunk, nwg;
 };
-// Workgroups of four waves per CU that the registers of a variant leave room for.
+// Workgroups of four waves per CU: two, or one where two would not leave a wave the registers for
+// its outputs and the blocks on their way (a spilled token loop runs at half the rate: 64 queries on
+// 256 channels 510 us with two, 186 us with one; three for the narrow ones gain nothing).
 constexpr int kv_occ(int D, bool fp8, int RB)
 {
-    return D == 64 ? (RB == 1 ? 4 : 3) : (D == 128 ? (RB == 1 ? (fp8 ? 4 : 3) : 2) : 2);
+    return D == 256 || (D == 128 && RB == 2 && !fp8) ? 1 : 2;
 }
 KvPlan kv_attention_plan(int D, bool fp8, int rows);
 // One translation unit per io and cache type.

@@ -42,7 +42,15 @@ constexpr int KV_TILE = 128;                 // tokens of a work unit
 constexpr int KV_SUB = 32;                   // tokens a wave takes at once
 constexpr float KV_SLACK = 5.f;              // powers of two a weight may pass its reference by
 constexpr int KV_OROW = 132;                 // floats per row of the join buffer (128 + padding)
-constexpr int KV_MAX_GROUPS = 4096;          // sequences of a call (the prefix array in LDS)
+constexpr int KV_MAX_WG = 1024;              // workgroups of a call
+
+// x, but not to the compiler: what is computed from it stays where it is written, instead of
+// being carried in registers through the token loop.
+__device__ __forceinline__ int kv_opaque(int x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
+}
 
 template <int IO>
 struct KvOp {                                // matrix operand: eight io elements
@@ -111,9 +119,16 @@ __device__ __forceinline__ KvRange kv_range(const KvAttention& a, int end, bool 
     return r;
 }
 
-// First unit of workgroup w, and the workgroup of unit u: the even cut of N units over W.
-__device__ __forceinline__ int kv_cut(long long N, int W, int w) { return (int)(N * w / W); }
-__device__ __forceinline__ int kv_owner(long long N, int W, long long u) { return (int)(((u + 1) * W - 1) / N); }
+// The even cut of N units over W workgroups: the first N % W take one more than the others.
+struct KvCut {
+    int each, more;                          // N / W, N % W
+    __device__ __forceinline__ int first(int w) const { return w * each + min(w, more); }
+    __device__ __forceinline__ int owner(int u) const
+    {
+        const int head = more * (each + 1);
+        return u < head ? u / (each + 1) : more + (u - head) / each;
+    }
+};
 
 // Result of a row: outputs of eight consecutive channels.
 template <int IO>
@@ -148,7 +163,12 @@ __global__ __launch_bounds__(256, OCC) void kv_attention_kernel(KvAttention a)
     constexpr float OFF = IO == KV_F16 ? 10.f : 0.f;  // fp16 weights stay clear of its subnormals
 
     extern __shared__ int s_pre[];
-    __shared__ float s_o[4][16][KV_OROW];
+    // the waves' queries in operand order while tokens pass, their outputs when they are joined
+    __shared__ union {
+        u32x4 q[4][RB * KS][64];
+        float o[4][16][KV_OROW];
+    } sh;
+    auto& s_o = sh.o;
     __shared__ float s_m[4][16], s_l[4][16];
     __shared__ int s_wave[4];
 
@@ -188,20 +208,16 @@ __global__ __launch_bounds__(256, OCC) void kv_attention_kernel(KvAttention a)
     }
     // at most a unit each, so that no workgroup inside a split range is without one
     const int N = uni(s_pre[a.B]), W = min((int)gridDim.x, N);
-    if (tid == 0) a.meta[4 * blockIdx.x] = -1;
+    const bool by_range = a.B * hc <= (int)gridDim.x;
+    if (!by_range && tid == 0) a.meta[2 * blockIdx.x] = -1;
     if ((int)blockIdx.x >= W) return;
-    int u = uni(kv_cut(N, W, blockIdx.x));
-    const int u1 = uni(kv_cut(N, W, blockIdx.x + 1));
-    int b;
-    {                                        // the sequence of unit u
-        int lo = 0, hi = a.B - 1;            // s_pre[lo] <= u < s_pre[hi + 1]
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (s_pre[mid + 1] <= u) lo = mid + 1;
-            else hi = mid;
-        }
-        b = uni(lo);
-    }
+    const KvCut cut{N / W, N % W};
+    int u = cut.first(blockIdx.x);
+    const int u1 = u + cut.each + ((int)blockIdx.x < cut.more ? 1 : 0);
+    for (int i = tid; i < a.B; i += 256)
+        if (s_pre[i] <= u && u < s_pre[i + 1]) s_wave[0] = i;
+    __syncthreads();
+    int b = uni(s_wave[0]);                  // the sequence of unit u
 
 #pragma unroll 1
     while (u < u1) {
@@ -214,25 +230,9 @@ __global__ __launch_bounds__(256, OCC) void kv_attention_kernel(KvAttention a)
         const int tend = min(rng.base + tb * KV_TILE, end);
         const int32_t* table = a.table + (size_t)b * a.max_pages;
 
-        // ---- queries: row n of each of the wave's blocks, eight channels of each product
-        u32x4 qf[RB][KS];
-        int lim_hi[RB], lim_lo[RB];          // visible positions of the row
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-            const int row = chunk * a.rpc + (rg * RB + rb) * 16 + n;
-            const int t = row / a.group, h = hkv * a.group + row - t * a.group;
-            const bool real = row < a.rows && (rg * RB + rb) * 16 + n < a.rpc;
-            lim_hi[rb] = real ? end - a.T + t + 1 : end;
-            lim_lo[rb] = real && a.window > 0 ? max(0, lim_hi[rb] - a.window) : 0;
-            const uint16_t* q = static_cast<const uint16_t*>(a.q) + ((size_t)t * a.B + b) * a.q_stride + (size_t)h * D;
-#pragma unroll
-            for (int i = 0; i < KS; ++i) {
-                // the channels of K's loads: eight at a time, or halves of sixteen codes
-                const int d = FP8 ? (i >> 1) * 64 + g * 16 + (i & 1) * 8 : i * 32 + g * 8;
-                qf[rb][i] = real ? *reinterpret_cast<const u32x4*>(q + d) : u32x4{0, 0, 0, 0};
-            }
-        }
         const float sc = FP8 ? a.scale_log2 * uload(a.k_scale + hkv) : a.scale_log2;
+        const float sc_abs = __builtin_fabsf(sc);
+        int lim_hi[RB], lim_lo[RB];          // visible positions of the row
 
         float m[RB], l[RB];
         f32x4 O[RB][JN];
@@ -258,11 +258,12 @@ __global__ __launch_bounds__(256, OCC) void kv_attention_kernel(KvAttention a)
 
         u32x4 kf[2][KL];
         uint32_t vf[2][4][VL][VW];
-        // Byte offset in the cache of the 16 tokens at t.  The page number is held inside the cache
-        // whatever the table says; positions whose entry is wrong are masked below.
-        auto locate = [&](int t) {
+        // Page and byte offset in the cache of the 16 tokens at t.  The page number is held inside the
+        // cache whatever the table says; positions whose entry is wrong are masked below.
+        auto page_of = [&](int t) { return (uint32_t)uload(table + (min(t, end - 1) >> a.page_shift)); };
+        auto locate = [&](uint32_t entry, int t) {
             const int at = min(t, end - 1);
-            const uint32_t page = min((uint32_t)uload(table + (at >> a.page_shift)), (uint32_t)a.npages - 1);
+            const uint32_t page = min(entry, (uint32_t)a.npages - 1);
             return wave_uniform(page * page_bytes + (size_t)((at & ~15) & ((1 << a.page_shift) - 1)) * (D * EB));
         };
         auto load_k = [&](size_t b0, size_t b1) {
@@ -297,10 +298,14 @@ __global__ __launch_bounds__(256, OCC) void kv_attention_kernel(KvAttention a)
         };
         // scores of the 32 tokens in kf (raw products)
         auto scores = [&](f32x4 (&s)[RB][2]) {
+            asm volatile("" ::: "memory");       // queries stay in LDS from block to block
 #pragma unroll
             for (int rb = 0; rb < RB; ++rb) s[rb][0] = s[rb][1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < KS; ++i)
+            for (int i = 0; i < KS; ++i) {
+                u32x4 qf[RB];
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb) qf[rb] = sh.q[wv][rb * KS + i][lane];
 #pragma unroll
                 for (int blk = 0; blk < 2; ++blk) {
                     u32x4 A;
@@ -313,8 +318,9 @@ __global__ __launch_bounds__(256, OCC) void kv_attention_kernel(KvAttention a)
                         A = kf[blk][i];
                     }
 #pragma unroll
-                    for (int rb = 0; rb < RB; ++rb) s[rb][blk] = kv_mfma<IO>(A, qf[rb][i], s[rb][blk]);
+                    for (int rb = 0; rb < RB; ++rb) s[rb][blk] = kv_mfma<IO>(A, qf[rb], s[rb][blk]);
                 }
+            }
         };
         // Scores to weights (hi + lo), with the running reference, sum and outputs kept in step.
         // see: which of the lane's eight tokens row block rb's row sees.
@@ -323,10 +329,9 @@ __global__ __launch_bounds__(256, OCC) void kv_attention_kernel(KvAttention a)
             for (int rb = 0; rb < RB; ++rb) {
                 float top = -INFINITY;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float x = s[rb][e >> 2][e & 3] * sc;
-                    top = fmaxf(top, !decltype(masked)::value || (see[rb] >> e & 1) ? x : -INFINITY);
-                }
+                for (int e = 0; e < 8; ++e)
+                    top = fmaxf(top, !decltype(masked)::value || (see[rb] >> e & 1) ? s[rb][e >> 2][e & 3] : -INFINITY);
+                top *= sc_abs;
                 if (__builtin_amdgcn_ballot_w64(top > m[rb] + (OFF + KV_SLACK)) != 0) {
                     // the row's maximum over the 32 tokens; its four lanes agree on the reference
                     const float mx = max_over_row_groups(top);
@@ -346,7 +351,7 @@ __global__ __launch_bounds__(256, OCC) void kv_attention_kernel(KvAttention a)
                     for (int k = 0; k < 2; ++k) {
                         const int e = 2 * i + k;
                         // one rounding between the score and its exponent
-                        p[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[rb][e >> 2][e & 3], sc, -ref));
+                        p[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[rb][e >> 2][e & 3], sc_abs, -ref));
                         if constexpr (decltype(masked)::value) p[k] = (see[rb] >> e & 1) ? p[k] : 0.f;
                         l[rb] += p[k];
                     }
@@ -365,6 +370,7 @@ __global__ __launch_bounds__(256, OCC) void kv_attention_kernel(KvAttention a)
                     if constexpr (decltype(some)::value) O[rb][j] = mine[rb] ? x : O[rb][j];
                     else O[rb][j] = x;
                 }
+                if constexpr (decltype(some)::value) __builtin_amdgcn_sched_barrier(0);
             };
 #pragma unroll
             for (int v = 0; v < VL; ++v) {
@@ -402,136 +408,162 @@ __global__ __launch_bounds__(256, OCC) void kv_attention_kernel(KvAttention a)
             }
         };
 
-        // ---- a table entry outside the cache sends the whole range through the masked path
+        // ---- the first block's keys and values are requested before anything is waited for
+        const int nb = t_first < tend ? (tend - t_first + step - 1) / step : 0;     // the wave's blocks
+        int t0 = t_first;
+        uint32_t p0 = 0, p1 = 0, c0 = 0, c1 = 0;     // table entries of the next and of the current block
+        size_t b0 = 0, b1 = 0;
+        if (nb > 0) {
+            c0 = page_of(t0);
+            c1 = page_of(t0 + 16);
+            b0 = locate(c0, t0);
+            b1 = locate(c1, t0 + 16);
+            load_k(b0, b1);
+            load_v(b0, b1);
+            p0 = page_of(t0 + step);
+            p1 = page_of(t0 + step + 16);
+        }
+
+        // ---- queries: row n of each of the wave's blocks, eight channels of each product.  Each wave
+        // keeps its own copy in LDS; the barrier keeps it behind the previous range's join.
+        __syncthreads();
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) {
+            const int nn = kv_opaque(lane & 15), row = chunk * a.rpc + (rg * RB + rb) * 16 + nn;
+            const int t = row / a.group, h = hkv * a.group + row - t * a.group;
+            const bool real = row < a.rows && (rg * RB + rb) * 16 + nn < a.rpc;
+            lim_hi[rb] = real ? end - a.T + t + 1 : end;
+            lim_lo[rb] = real && a.window > 0 ? max(0, lim_hi[rb] - a.window) : 0;
+            const uint16_t* q = static_cast<const uint16_t*>(a.q) + ((size_t)t * a.B + b) * a.q_stride + (size_t)h * D;
+            const uint32_t flip = sc < 0.f ? 0x80008000u : 0u;      // scores are scaled by |sc|
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+                // the channels of K's loads: eight at a time, or halves of sixteen codes
+                const int d = FP8 ? (i >> 1) * 64 + g * 16 + (i & 1) * 8 : i * 32 + g * 8;
+                u32x4 w = real ? *reinterpret_cast<const u32x4*>(q + d) : u32x4{0, 0, 0, 0};
+                w ^= u32x4{flip, flip, flip, flip};
+                sh.q[wv][rb * KS + i][lane] = w;
+            }
+        }
+        // a table entry outside the cache sends the whole range through the masked path
         bool wrong = false;
-        for (int i = ((rng.base + ta * KV_TILE) >> a.page_shift) + lane; i < (tend + (1 << a.page_shift) - 1) >> a.page_shift; i += 64)
+        for (int i = ((rng.base + ta * KV_TILE) >> a.page_shift) + lane;
+             i < (tend + (1 << a.page_shift) - 1) >> a.page_shift; i += 64)
             wrong |= (uint32_t)table[i] >= (uint32_t)a.npages;
         wrong = __builtin_amdgcn_ballot_w64(wrong) != 0;
         if (wrong && lane == 0 && a.err) atomicOr(a.err, KVERR_BAD_SLOT);
 
-        // ---- tokens that every row sees: [all_lo, all_hi)
-        const int f0 = t_first >= all_lo ? t_first : t_first + (all_lo - t_first + step - 1) / step * step;
-        const int f1 = wrong ? f0 : min(tend, all_hi) - KV_SUB + 1;              // first tokens of whole blocks: < f1
-        if (f0 < f1) {
-            int t0 = f0;
-            size_t b0 = locate(t0), b1 = locate(t0 + 16);
-            load_k(b0, b1);
-            load_v(b0, b1);
-#pragma unroll 1
-            while (true) {
-                f32x4 s[RB][2];
-                scores(s);
-                t0 += step;
-                const bool more = t0 < f1;
-                if (more) {
-                    b0 = locate(t0);
-                    b1 = locate(t0 + 16);
-                    load_k(b0, b1);
-                }
-                u32x4 ph[RB], pl[RB];
-                const uint32_t all[RB] = {};
-                const bool every[RB] = {};
-                weights(s, all, std::false_type{}, ph, pl);
-                outputs(ph, pl, std::false_type{}, every);
-                if (!more) break;
-                load_v(b0, b1);
-            }
-        }
-
-        // ---- the other blocks: ends of the sequence, of the drafts and of their windows
-#pragma unroll 1
-        for (int t0 = t_first; t0 < tend; t0 += step) {
-            if (t0 >= f0 && t0 < f1) {
-                t0 += (f1 - 1 - t0) / step * step;
-                continue;
-            }
-            const size_t b0 = locate(t0), b1 = locate(t0 + 16);
-            const int e0 = table[min(t0, end - 1) >> a.page_shift], e1 = table[min(t0 + 16, end - 1) >> a.page_shift];
-            const bool ok0 = (uint32_t)e0 < (uint32_t)a.npages, ok1 = (uint32_t)e1 < (uint32_t)a.npages;
-            load_k(b0, b1);
+        // ---- tokens.  Every block but the last requests the next one unconditionally: the waits for K
+        // and V then count exactly the requests behind them.
+        auto block = [&](auto more) {
             f32x4 s[RB][2];
             scores(s);
-            uint32_t see[RB];
-#pragma unroll
-            for (int rb = 0; rb < RB; ++rb) {
-                see[rb] = 0;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int t = t0 + (e >> 2) * 16 + 4 * g + (e & 3);
-                    if (t < lim_hi[rb] && t >= lim_lo[rb] && (e < 4 ? ok0 : ok1)) see[rb] |= 1u << e;
-                }
+            const int cur = t0;
+            const size_t cb0 = b0, cb1 = b1;
+            const bool ok0 = c0 < (uint32_t)a.npages, ok1 = c1 < (uint32_t)a.npages;
+            if constexpr (decltype(more)::value) {
+                t0 += step;
+                c0 = p0;
+                c1 = p1;
+                b0 = locate(c0, t0);
+                b1 = locate(c1, t0 + 16);
+                load_k(b0, b1);
+                p0 = page_of(t0 + step);
+                p1 = page_of(t0 + step + 16);
+                __builtin_amdgcn_sched_barrier(0);
             }
             u32x4 ph[RB], pl[RB];
-            weights(s, see, std::true_type{}, ph, pl);
-            // Values that no row sees count as zero, so that 0 * NaN does not arise.  A value that only
-            // some drafts see and that is no number would still reach the others: then, and only then,
-            // the drafts are taken one by one.
-            bool apart = false;
+            uint32_t see[RB] = {};
+            bool mine[RB] = {};
+            if (!wrong && cur >= all_lo && cur + KV_SUB <= all_hi) {        // every row sees every token
+                weights(s, see, std::false_type{}, ph, pl);
+                outputs(ph, pl, std::false_type{}, mine);
+            } else {
+                const int mt = cur + 4 * kv_opaque(g);                      // the lane's first token
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int t = mt + (e >> 2) * 16 + (e & 3);
+                        if (t < lim_hi[rb] && t >= lim_lo[rb] && (e < 4 ? ok0 : ok1)) see[rb] |= 1u << e;
+                    }
+                }
+                weights(s, see, std::true_type{}, ph, pl);
+                // Values that no row sees count as zero, so that 0 * NaN does not arise.  A value that only
+                // some drafts see and that is no number would still reach the others: then, and only then,
+                // the drafts are taken one by one.
+                auto clear = [&](int lo, int hi) {
+                    uint32_t odd = 0;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int t = mt + (e >> 2) * 16 + (e & 3);
+                        const bool sees = t < hi && t >= lo && (e < 4 ? ok0 : ok1);
+                        const bool some = t < all_lo || t >= all_hi;
+#pragma unroll
+                        for (int v = 0; v < VL; ++v)
+#pragma unroll
+                            for (int w = 0; w < VW; ++w) {
+                                const uint32_t x = sees ? vf[e >> 2][e & 3][v][w] : 0u;
+                                vf[e >> 2][e & 3][v][w] = x;
+                                if (some) odd |= kv_odd<IO, FP8>(x);
+                            }
+                    }
+                    return __builtin_amdgcn_ballot_w64(odd != 0) != 0;
+                };
+                const bool odd = clear(a.window > 0 ? max(0, end - a.T + 1 - a.window) : 0, end);
+                if (a.T == 1 || !odd) {
+                    outputs(ph, pl, std::false_type{}, mine);
+                } else {
 #pragma unroll 1
-            for (int d = -1; d < (apart ? a.T : 0); ++d) {
-                const int hi = d < 0 ? end : end - a.T + d + 1;
-                const int lo = a.window > 0 ? max(0, (d < 0 ? end - a.T + 1 : hi) - a.window) : 0;
-                load_v(b0, b1);
-                uint32_t odd = 0;
+                    for (int d = 0; d < a.T; ++d) {
+                        const int hi = end - a.T + d + 1;
+                        load_v(cb0, cb1);
+                        clear(a.window > 0 ? max(0, hi - a.window) : 0, hi);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int t = t0 + (e >> 2) * 16 + 4 * g + (e & 3);
-                    const bool sees = t < hi && t >= lo && (e < 4 ? ok0 : ok1);
-                    const bool some = t < all_lo || t >= all_hi;
-#pragma unroll
-                    for (int v = 0; v < VL; ++v)
-#pragma unroll
-                        for (int w = 0; w < VW; ++w) {
-                            const uint32_t x = sees ? vf[e >> 2][e & 3][v][w] : 0u;
-                            vf[e >> 2][e & 3][v][w] = x;
-                            if (some) odd |= kv_odd<IO, FP8>(x);
-                        }
+                        for (int rb = 0; rb < RB; ++rb) mine[rb] = lim_hi[rb] == hi;
+                        outputs(ph, pl, std::true_type{}, mine);
+                    }
                 }
-                if (d < 0) {
-                    apart = a.T > 1 && __builtin_amdgcn_ballot_w64(odd != 0) != 0;
-                    if (apart) continue;
-                }
-                bool mine[RB];
-#pragma unroll
-                for (int rb = 0; rb < RB; ++rb) mine[rb] = d < 0 || lim_hi[rb] == hi;
-                outputs(ph, pl, std::true_type{}, mine);
             }
+            if constexpr (decltype(more)::value) {
+                load_v(b0, b1);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        if (nb > 0) {
+#pragma unroll 1
+            for (int left = nb - 1; left > 0; --left) block(std::true_type{});
+            block(std::false_type{});
         }
 
         // ---- join the waves of each row group; whole ranges write the output
         const bool whole = ta == 0 && tb == rng.tiles;
         const int slot = 2 * blockIdx.x + (ta == 0 ? 1 : 0);
         const float vs = FP8 ? uload(a.v_scale + hkv) : 1.f;
+        const int jt = kv_opaque(tid), jn = jt & 15, jg = (jt >> 4) & 3;
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb) {
             const float lw = sum_over_row_groups(l[rb]);
-            __syncthreads();
-            if (g == 0) {
-                s_m[wv][n] = m[rb];
-                s_l[wv][n] = lw;
-            }
-            __syncthreads();
-            float mx = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < NTW; ++i) mx = fmaxf(mx, s_m[i * RW + rg][n]);
-            const float f = m[rb] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[rb] - mx);
 #pragma unroll
             for (int jp = 0; jp < JN; jp += JP) {
-                if (jp > 0) __syncthreads();
+                __syncthreads();                                 // queries or the previous part are done with
+                if (jp == 0 && jg == 0) {
+                    s_m[wv][jn] = m[rb];
+                    s_l[wv][jn] = lw;
+                }
                 // lane: row n, channels VE (4 g + r).. of each load's 16 VE
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
 #pragma unroll
                     for (int j = 0; j < JP; j += 4) {
-                        const int jj = jp + j, d = (jj / VE) * 16 * VE + (4 * g + r) * VE + jj % VE;
+                        const int jj = jp + j, d = (jj / VE) * 16 * VE + (4 * jg + r) * VE + jj % VE;
                         // channel within the joined 16 JP: whole loads of 16 VE, or the halves of one
-                        const int c = VE <= JP ? d - jp * 16 : (4 * g + r) * JP + j;
-                        st4(&s_o[wv][n][c], f32x4{O[rb][jj][r] * f, O[rb][jj + 1][r] * f, O[rb][jj + 2][r] * f,
-                                                  O[rb][jj + 3][r] * f});
+                        const int c = VE <= JP ? d - jp * 16 : (4 * jg + r) * JP + j;
+                        st4(&s_o[wv][jn][c], f32x4{O[rb][jj][r], O[rb][jj + 1][r], O[rb][jj + 2][r], O[rb][jj + 3][r]});
                     }
                 __syncthreads();
                 constexpr int C8 = JP * 2;                       // eight-channel pieces of a row
-                for (int i = tid; i < RW * 16 * C8; i += 256) {
+                for (int i = jt; i < RW * 16 * C8; i += 256) {
                     const int rr = i / C8, c = (i - rr * C8) * 8, grp = rr >> 4, nn = rr & 15;
                     const int rl = (grp * RB + rb) * 16 + nn, row = chunk * a.rpc + rl;
                     if (rl >= a.rpc || row >= a.rows) continue;
@@ -542,12 +574,13 @@ __global__ __launch_bounds__(256, OCC) void kv_attention_kernel(KvAttention a)
 #pragma unroll
                     for (int k = 0; k < NTW; ++k) {
                         const float mk = s_m[k * RW + grp][nn];
-                        L += mk == -INFINITY ? s_l[k * RW + grp][nn] : s_l[k * RW + grp][nn] * __builtin_amdgcn_exp2f(mk - M);
+                        const float f = mk == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(mk - M);
+                        L += f * s_l[k * RW + grp][nn];
                         const f32x4 y0 = ld4(&s_o[k * RW + grp][nn][c]), y1 = ld4(&s_o[k * RW + grp][nn][c + 4]);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            x[e] += y0[e];
-                            x[4 + e] += y1[e];
+                            x[e] += f * y0[e];
+                            x[4 + e] += f * y1[e];
                         }
                     }
                     if (whole) {
@@ -568,70 +601,71 @@ __global__ __launch_bounds__(256, OCC) void kv_attention_kernel(KvAttention a)
                 }
             }
         }
-        if (tid == 0 && ta == 0 && tb < rng.tiles) {
-            int32_t* mt = a.meta + 4 * blockIdx.x;
-            mt[0] = b;
-            mt[1] = seg;
-            mt[2] = kv_owner(N, W, (long long)pre + (long long)(seg + 1) * rng.tiles - 1);   // last workgroup of the range
+        if (tid == 0 && ta == 0 && (by_range || !whole)) {
+            const int range = b * hc + seg;
+            int32_t* mt = a.meta + 2 * (by_range ? range : (int)blockIdx.x);
+            mt[0] = by_range ? (whole ? -1 : (int)blockIdx.x) : range;
+            mt[1] = cut.owner(pre + (seg + 1) * rng.tiles - 1);
         }
         u += tb - ta;
     }
 }
 
-// Joins the partial rows of one split range: blockIdx.x is the workgroup that opened it.
-// 256 threads: D / 4 lanes of four channels, 1024 / D groups of parts.
-template <int IO, bool FP8, int D>
+// Joins the partial rows of one split range, a row at a time.  blockIdx.x is the range where there
+// are no more of them than workgroups, else the workgroup that opened it.  The parts' references and sums first, each part's weight into LDS, then the outputs by 256
+// threads = D / 4 lanes of four channels x 1024 / D groups of parts.
+template <int IO, bool FP8, int D, bool BY_RANGE>
 __global__ __launch_bounds__(256) void kv_combine_kernel(KvAttention a)
 {
     constexpr int CL = D / 4, PG = 256 / CL;
-    __shared__ float s_x[PG][D], s_m[PG], s_l[PG];
-    const int w0 = blockIdx.x;
-    const int b = uload(a.meta + 4 * w0);
-    if (b < 0) return;
-    const int seg = uload(a.meta + 4 * w0 + 1), w1 = uload(a.meta + 4 * w0 + 2);
+    __shared__ float s_x[PG][D], s_w[KV_MAX_WG], s_m[4], s_l[4];
+    const int hc = a.Hkv * a.nchunk, found = uload(a.meta + 2 * blockIdx.x);
+    const int range = BY_RANGE ? blockIdx.x : found, w0 = BY_RANGE ? found : blockIdx.x;
+    const int b = max(range, 0) / hc, seg = range - b * hc;
+    if ((BY_RANGE && a.active && !uload(a.active + b)) || found < 0) return;
+    const int w1 = uload(a.meta + 2 * blockIdx.x + 1);
+    const int np = w1 - w0 + 1, tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
     const int hkv = seg / a.nchunk, chunk = seg - hkv * a.nchunk;
-    const int c = threadIdx.x % CL, pg = threadIdx.x / CL;
+    const int c = tid % CL, pg = tid / CL;
     const float vs = FP8 ? uload(a.v_scale + hkv) : 1.f;
     const int rows = min(a.rpc, a.rows - chunk * a.rpc);
+    // the opening workgroup's part is its last (slot 1), the others' their first (slot 0)
+    auto part = [&](int i, int rl) { return (size_t)(2 * (w0 + i) + (i == 0 ? 1 : 0)) * a.rpc + rl; };
     for (int rl = blockIdx.y; rl < rows; rl += gridDim.y) {
         float M = -INFINITY, L = 0.f;
-        f32x4 x = {0.f, 0.f, 0.f, 0.f};
-        for (int w = w0 + pg; w <= w1; w += PG) {
-            // the opening workgroup's part is its last (slot 1), the others' their first (slot 0)
-            const size_t at = (size_t)(2 * w + (w == w0 ? 1 : 0)) * a.rpc + rl;
-            const float m = a.part_ml[2 * at], l = a.part_ml[2 * at + 1];
-            const f32x4 y = ld4(a.part_o + at * D + 4 * c);
-            const float mn = fmaxf(M, m);
-            const float f0 = M == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(M - mn);
-            const float f1 = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn);
-            M = mn;
-            L = L * f0 + l * f1;
-            x = x * f0 + y * f1;
-        }
-        st4(&s_x[pg][4 * c], x);
-        if (c == 0) {
-            s_m[pg] = M;
-            s_l[pg] = L;
-        }
-        __syncthreads();
-        float MM = -INFINITY, LL = 0.f;
+        for (int i = tid; i < np; i += 256) M = fmaxf(M, a.part_ml[2 * part(i, rl)]);
 #pragma unroll
-        for (int k = 0; k < PG; ++k) MM = fmaxf(MM, s_m[k]);
-        if (threadIdx.x < D / 8) {
+        for (int o = 32; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor(M, o, 64));
+        if (lane == 0) s_m[wv] = M;
+        __syncthreads();
+        M = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+        for (int i = tid; i < np; i += 256) {
+            const float m = a.part_ml[2 * part(i, rl)];
+            const float f = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - M);
+            s_w[i] = f;
+            L += f * a.part_ml[2 * part(i, rl) + 1];
+        }
+        L = wave_sum64(L);
+        if (lane == 0) s_l[wv] = L;
+        __syncthreads();
+        f32x4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+        for (int i = pg; i < np; i += PG) x += ld4(a.part_o + part(i, rl) * D + 4 * c) * s_w[i];
+        st4(&s_x[pg][4 * c], x);
+        __syncthreads();
+        if (tid < D / 8) {
+            L = s_l[0] + s_l[1] + s_l[2] + s_l[3];
             float y[8] = {};
 #pragma unroll
-            for (int k = 0; k < PG; ++k) {
-                const float f = s_m[k] == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(s_m[k] - MM);
-                LL += s_l[k] * f;
+            for (int k = 0; k < PG; ++k)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] += s_x[k][8 * threadIdx.x + e] * f;
-            }
-            const float inv = LL == 0.f ? 0.f : vs / LL;
+                for (int e = 0; e < 8; ++e) y[e] += s_x[k][8 * tid + e];
+            const float inv = L == 0.f ? 0.f : vs / L;
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] *= inv;
             const int row = chunk * a.rpc + rl;
-            kv_store_o<IO>(a, b, hkv, row, 8 * threadIdx.x, D, y);
-            if (threadIdx.x == 0) kv_store_lse(a, b, hkv, row, MM, LL);
+            kv_store_o<IO>(a, b, hkv, row, 8 * tid, D, y);
+            if (tid == 0) kv_store_lse(a, b, hkv, row, M, L);
         }
         __syncthreads();
     }
@@ -643,7 +677,10 @@ static hipError_t kv_attention_start(const KvAttention& a, const KvPlan& p, hipS
     hipLaunchKernelGGL((kv_attention_kernel<IO, FP8, D, RB, RW, OCC>), dim3(p.nwg), dim3(256), (a.B + 1) * sizeof(int), s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((kv_combine_kernel<IO, FP8, D>), dim3(p.nwg, p.rpc < 16 ? p.rpc : 16), dim3(256), 0, s, a);
+    const int ranges = a.B * a.Hkv * a.nchunk, most = ranges <= p.nwg ? ranges : p.nwg;
+    const int y = p.rpc < 8192 / most ? p.rpc : 8192 / most;         // rows side by side, within some waves of the chip
+    if (ranges <= p.nwg) hipLaunchKernelGGL((kv_combine_kernel<IO, FP8, D, true>), dim3(ranges, y), dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((kv_combine_kernel<IO, FP8, D, false>), dim3(p.nwg, y), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
