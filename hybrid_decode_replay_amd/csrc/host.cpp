@@ -15,20 +15,20 @@
 
 namespace rs {
 
-// Rows that share a key/value head fill 16-row products; a wave takes one or two such blocks, and
-// past 32 rows the waves of a workgroup take different rows over the same tokens, so that the
-// cache is still read once.  Wide heads keep to one block a wave (two would leave one wave per
-// SIMD).  More rows than a workgroup holds make further chunks, which read the cache again.
+// Rows that share a key/value head fill 16-row products.  Up to 32 rows a wave takes one or two such
+// blocks and the waves of a workgroup split the tokens; past that the cache goes through LDS and the
+// waves take different rows.  Wide heads have one block a wave there (registers).  More rows than a
+// workgroup holds make further chunks, which read the cache again.
 KvPlan kv_attention_plan(int D, bool fp8, int rows)
 {
     KvPlan p;
-    p.RB = D == 256 || rows <= 16 ? 1 : 2;
-    const int groups = (rows + 16 * p.RB - 1) / (16 * p.RB);
-    p.RW = groups <= 1 ? 1 : (groups == 2 ? 2 : 4);
-    const int most = 16 * p.RB * p.RW;
+    p.wide = rows > 32;
+    const int block = p.wide ? 64 : 16;
+    p.RB = rows <= block || (p.wide && D == 256) ? 1 : 2;
+    const int most = block * p.RB;
     p.rpc = rows < most ? rows : most;
     p.nchunk = (rows + most - 1) / most;
-    p.nwg = 256 * kv_occ(D, fp8, p.RB);
+    p.nwg = 256 * (p.wide ? 1 : kv_occ(D, fp8, p.RB));
     return p;
 }
 

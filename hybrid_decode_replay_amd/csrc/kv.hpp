@@ -56,14 +56,16 @@ struct KvAttention {
     float* part_o;           // [2 nwg][rpc][D]
     int B, Hq, Hkv, group, T, npages, page_shift, max_pages, window;
     int rows;                // T * group rows share a key/value head
-    int rpc;                 // rows of a chunk, at most 16 RB RW
+    int rpc;                 // rows of a chunk, at most 16 RB (64 RB in the wide kernel)
     int nchunk;              // chunks of rows
     float scale_log2;        // scale * log2(e)
 };
-// How a call is cut: row blocks of 16 per wave, row groups of waves per
-// workgroup, workgroups.  The rule stands at kv_attention_plan.
+// How a call is cut: row blocks of 16 per wave, the kernel for many rows or for few, rows of a
+// chunk, chunks, workgroups.  The rule stands at kv_attention_plan.
 struct KvPlan {
-    int RB, RW, rpc, nchunk, nwg;
+    int RB;
+    bool wide;
+    int rpc, nchunk, nwg;
 };
 // Workgroups of four waves per CU: two, or one where two would not leave a wave the registers for
 // its outputs and the blocks on their way (a spilled token loop runs at half the rate: 64 queries on

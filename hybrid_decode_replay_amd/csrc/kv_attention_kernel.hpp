@@ -41,7 +41,6 @@ namespace rs {
 constexpr int KV_TILE = 128;                 // tokens of a work unit
 constexpr int KV_SUB = 32;                   // tokens a wave takes at once
 constexpr float KV_SLACK = 5.f;              // powers of two a weight may pass its reference by
-constexpr int KV_OROW = 132;                 // floats per row of the join buffer (128 + padding)
 constexpr int KV_MAX_WG = 1024;              // workgroups of a call
 
 // x, but not to the compiler: what is computed from it stays where it is written, instead of
@@ -97,12 +96,25 @@ __device__ __forceinline__ uint32_t kv_odd(uint32_t w)
     }
 }
 
-// A load of the cache's stream: past the caches unless the waves of a workgroup share it.
-template <bool STREAM, typename T>
-__device__ __forceinline__ T kv_load(const uint8_t* p)
+// A load of the cache's stream (used once: past the caches).
+template <typename T>
+__device__ __forceinline__ T kv_stream(const uint8_t* p)
 {
-    if constexpr (STREAM) return __builtin_nontemporal_load(reinterpret_cast<const T*>(p));
-    else return *reinterpret_cast<const T*>(p);
+    return __builtin_nontemporal_load(reinterpret_cast<const T*>(p));
+}
+// N consecutive words, from the stream or from LDS.
+template <int N, bool STREAM>
+__device__ __forceinline__ void kv_words(const uint8_t* p, uint32_t (&w)[N])
+{
+    using T = typename std::conditional<N == 4, u32x4, typename std::conditional<N == 2, u32x2, uint32_t>::type>::type;
+    T x;
+    if constexpr (STREAM) x = kv_stream<T>(p);
+    else x = *reinterpret_cast<const T*>(p);
+    if constexpr (N == 1) w[0] = x;
+    else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = x[i];
+    }
 }
 
 // First and last visible position of a sequence's rows and its tiles.
@@ -130,14 +142,15 @@ struct KvCut {
     }
 };
 
-// Result of a row: outputs of eight consecutive channels.
-template <int IO>
+// Result of a row: outputs of four or eight consecutive channels.
+template <int IO, int N>
 __device__ __forceinline__ void kv_store_o(const KvAttention& a, int b, int hkv, int row, int d, int D,
-                                           const float (&x)[8])
+                                           const float (&x)[N])
 {
     const int t = row / a.group, h = hkv * a.group + row - t * a.group;
     uint16_t* o = static_cast<uint16_t*>(a.o) + (((size_t)t * a.B + b) * a.Hq + h) * D + d;
-    *reinterpret_cast<u32x4*>(o) = kv_pack8<IO>(x);
+    if constexpr (N == 8) *reinterpret_cast<u32x4*>(o) = kv_pack8<IO>(x);
+    else *reinterpret_cast<u32x2*>(o) = u32x2{kv_pack<IO>(x[0], x[1]), kv_pack<IO>(x[2], x[3])};
 }
 __device__ __forceinline__ void kv_store_lse(const KvAttention& a, int b, int hkv, int row, float m, float l)
 {
@@ -146,96 +159,152 @@ __device__ __forceinline__ void kv_store_lse(const KvAttention& a, int b, int hk
     a.lse[((size_t)t * a.B + b) * a.Hq + h] = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
 }
 
-// D channels, RB blocks of 16 rows per wave, RW groups of waves with rows of their own (the 4 / RW
-// waves of a group share its tokens).  Shared memory: prefix sums [B + 1] (dynamic).
-template <int IO, bool FP8, int D, int RB, int RW, int OCC>
-__global__ __launch_bounds__(256, OCC) void kv_attention_kernel(KvAttention a)
+// Sizes that follow from the cached type and the width of a head.
+template <bool FP8, int D>
+struct KvGeom {
+    static constexpr int EB = FP8 ? 1 : 2;               // bytes of a cached value
+    static constexpr int ROWB = D * EB;                  // bytes of a token's head
+    static constexpr int KS = D / 32;                    // products along a head
+    static constexpr int JN = D / 16;                    // 16-channel groups of the output
+    static constexpr int VE = JN < 16 / EB ? JN : 16 / EB;   // channels a lane takes of a token at once
+    static constexpr int VL = JN / VE;                   // such pieces per token
+    static constexpr int VW = VE * EB / 4;               // words of such a piece
+    static constexpr int KL = ROWB / 64;                 // 16-byte pieces of K per token and lane
+};
+
+// The line of units as a workgroup sees it, and its place on it.
+struct KvLine {
+    int hc, u, u1, b;                        // ranges per sequence; first and last + 1 unit; sequence of the first
+    bool by_range;
+    KvCut cut;
+};
+
+// Prefix sums of tiles over the batch into s_pre [B + 1], and this workgroup's units; false if it
+// has none.  `tmp` holds an entry per wave.
+template <int NT>
+__device__ __forceinline__ bool kv_line(const KvAttention& a, int* s_pre, int* tmp, KvLine& ln)
 {
-    constexpr int NTW = 4 / RW;              // waves that split a row group's tokens
-    constexpr int KS = D / 32;               // products along a head
-    constexpr int JN = D / 16;               // 16-channel groups of the output
-    constexpr int EB = FP8 ? 1 : 2;          // bytes of a cached value
-    constexpr int VE = JN < 16 / EB ? JN : 16 / EB;   // channels a lane loads of a token at once
-    constexpr int VL = JN / VE;              // such loads per token
-    constexpr int VW = VE * EB / 4;          // words of such a load
-    constexpr int KL = D * EB / 64;          // 16-byte loads of K per token and lane
-    constexpr int JP = JN < 8 ? JN : 8;      // 16-channel groups joined at once
-    constexpr float OFF = IO == KV_F16 ? 10.f : 0.f;  // fp16 weights stay clear of its subnormals
-
-    extern __shared__ int s_pre[];
-    // the waves' queries in operand order while tokens pass, their outputs when they are joined
-    __shared__ union {
-        u32x4 q[4][RB * KS][64];
-        float o[4][16][KV_OROW];
-    } sh;
-    auto& s_o = sh.o;
-    __shared__ float s_m[4][16], s_l[4][16];
-    __shared__ int s_wave[4];
-
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wv = uni(tid >> 6), rg = wv % RW, tw = wv / RW;
-    const int n = lane & 15, g = lane >> 4;
-    const int hc = a.Hkv * a.nchunk;
-
-    // ---- the line of units: prefix sums of tiles over the batch
-    {
-        int carry = 0;
-        for (int b0 = 0; b0 < a.B; b0 += 256) {
-            const int b = b0 + tid;
-            int v = 0;
-            if (b < a.B) {
-                const int e = a.end[b];
-                v = kv_range(a, e, !a.active || a.active[b]).tiles * hc;
-                if (blockIdx.x == 0 && a.err && (e < 0 || e > (a.max_pages << a.page_shift))) atomicOr(a.err, KVERR_BAD_SLOT);
-            }
-#pragma unroll
-            for (int o = 1; o < 64; o <<= 1) {
-                const int u = __shfl_up(v, o, 64);
-                if (lane >= o) v += u;
-            }
-            if (lane == 63) s_wave[wv] = v;
-            __syncthreads();
-            int before = carry;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (i < wv) before += s_wave[i];
-                carry += s_wave[i];
-            }
-            if (b < a.B) s_pre[b + 1] = before + v;
-            if (b == 0) s_pre[0] = 0;
-            __syncthreads();
+    const int tid = threadIdx.x, lane = tid & 63, wv = uni(tid >> 6);
+    ln.hc = a.Hkv * a.nchunk;
+    int carry = 0;
+    for (int b0 = 0; b0 < a.B; b0 += NT) {
+        const int b = b0 + tid;
+        int v = 0;
+        if (b < a.B) {
+            const int e = a.end[b];
+            v = kv_range(a, e, !a.active || a.active[b]).tiles * ln.hc;
+            if (blockIdx.x == 0 && a.err && (e < 0 || e > (a.max_pages << a.page_shift))) atomicOr(a.err, KVERR_BAD_SLOT);
         }
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int x = __shfl_up(v, o, 64);
+            if (lane >= o) v += x;
+        }
+        if (lane == 63) tmp[wv] = v;
+        __syncthreads();
+        int before = carry;
+#pragma unroll
+        for (int i = 0; i < NT / 64; ++i) {
+            if (i < wv) before += tmp[i];
+            carry += tmp[i];
+        }
+        if (b < a.B) s_pre[b + 1] = before + v;
+        if (b == 0) s_pre[0] = 0;
+        __syncthreads();
     }
     // at most a unit each, so that no workgroup inside a split range is without one
     const int N = uni(s_pre[a.B]), W = min((int)gridDim.x, N);
-    const bool by_range = a.B * hc <= (int)gridDim.x;
-    if (!by_range && tid == 0) a.meta[2 * blockIdx.x] = -1;
-    if ((int)blockIdx.x >= W) return;
-    const KvCut cut{N / W, N % W};
-    int u = cut.first(blockIdx.x);
-    const int u1 = u + cut.each + ((int)blockIdx.x < cut.more ? 1 : 0);
-    for (int i = tid; i < a.B; i += 256)
-        if (s_pre[i] <= u && u < s_pre[i + 1]) s_wave[0] = i;
+    ln.by_range = a.B * ln.hc <= (int)gridDim.x;
+    if (!ln.by_range && tid == 0) a.meta[2 * blockIdx.x] = -1;
+    if ((int)blockIdx.x >= W) return false;
+    const int each = uni(N / W);
+    ln.cut = KvCut{each, N - each * W};
+    ln.u = ln.cut.first(blockIdx.x);
+    ln.u1 = ln.u + ln.cut.each + ((int)blockIdx.x < ln.cut.more ? 1 : 0);
+    for (int i = tid; i < a.B; i += NT)
+        if (s_pre[i] <= ln.u && ln.u < s_pre[i + 1]) tmp[0] = i;
     __syncthreads();
-    int b = uni(s_wave[0]);                  // the sequence of unit u
+    ln.b = uni(tmp[0]);
+    return true;
+}
 
-#pragma unroll 1
-    while (u < u1) {
-        while (uni(s_pre[b + 1]) <= u) ++b;
-        const KvRange rng = kv_range(a, uload(a.end + b), true);
-        const int pre = uni(s_pre[b]), seg = (u - pre) / rng.tiles;
-        const int ta = u - pre - seg * rng.tiles, tb = min(rng.tiles, ta + u1 - u);
-        const int hkv = seg / a.nchunk, chunk = seg - hkv * a.nchunk;
-        const int end = rng.end;
-        const int tend = min(rng.base + tb * KV_TILE, end);
-        const int32_t* table = a.table + (size_t)b * a.max_pages;
+// A workgroup's part of one range: tiles [ta, tb) of sequence b, key/value head hkv, row chunk.
+struct KvPart {
+    int b, seg, hkv, chunk, ta, tb, tiles, end, base, tend;
+    int all_lo, all_hi;                      // positions that every row sees
+    const int32_t* table;
+    float sc;                                // signed scale of the raw products, in powers of two
+    __device__ __forceinline__ bool whole() const { return ta == 0 && tb == tiles; }
+    // (a scale of zero would let masked scores through: the smallest normal number stands for it)
+    __device__ __forceinline__ float sc_abs() const { return fmaxf(__builtin_fabsf(sc), 0x1p-126f); }
+    // every row sees every one of the n tokens at t
+    __device__ __forceinline__ bool full(int t, int n) const { return t >= all_lo && t + n <= all_hi; }
+};
+template <bool FP8>
+__device__ __forceinline__ KvPart kv_part(const KvAttention& a, const int* s_pre, KvLine& ln)
+{
+    KvPart p;
+    while (uni(s_pre[ln.b + 1]) <= ln.u) ++ln.b;
+    // everything to scalar registers: the loops over tokens then branch without masks
+    p.b = uni(ln.b);
+    const KvRange rng = kv_range(a, uload(a.end + p.b), true);
+    const int at = ln.u - uni(s_pre[p.b]);
+    p.tiles = uni(rng.tiles);
+    p.seg = uni(at / p.tiles);
+    p.ta = uni(at - p.seg * p.tiles);
+    p.tb = uni(min(p.tiles, p.ta + ln.u1 - ln.u));
+    p.hkv = uni(p.seg / a.nchunk);
+    p.chunk = uni(p.seg - p.hkv * a.nchunk);
+    p.end = uni(rng.end);
+    p.base = uni(rng.base);
+    p.tend = uni(min(p.base + p.tb * KV_TILE, p.end));
+    p.all_hi = uni(p.end - a.T + 1);
+    p.all_lo = uni(a.window > 0 ? max(0, p.end - a.window) : 0);
+    p.table = a.table + (size_t)p.b * a.max_pages;
+    p.sc = FP8 ? a.scale_log2 * uload(a.k_scale + p.hkv) : a.scale_log2;
+    return p;
+}
 
-        const float sc = FP8 ? a.scale_log2 * uload(a.k_scale + hkv) : a.scale_log2;
-        const float sc_abs = __builtin_fabsf(sc);
-        int lim_hi[RB], lim_lo[RB];          // visible positions of the row
+// Whether a table entry of the part lies outside the cache (its blocks then take the masked path).
+__device__ __forceinline__ bool kv_wrong_pages(const KvAttention& a, const KvPart& p, int lane)
+{
+    bool wrong = false;
+    for (int i = ((p.base + p.ta * KV_TILE) >> a.page_shift) + lane;
+         i < (p.tend + (1 << a.page_shift) - 1) >> a.page_shift; i += 64)
+        wrong |= (uint32_t)p.table[i] >= (uint32_t)a.npages;
+    wrong = __builtin_amdgcn_ballot_w64(wrong) != 0;
+    if (wrong && lane == 0 && a.err) atomicOr(a.err, KVERR_BAD_SLOT);
+    return wrong;
+}
 
-        float m[RB], l[RB];
-        f32x4 O[RB][JN];
+// Where the 16 tokens at t lie.  The page number is held inside the cache whatever the table says;
+// positions whose entry is wrong are masked.
+__device__ __forceinline__ uint32_t kv_page_of(const KvAttention& a, const KvPart& p, int t)
+{
+    return (uint32_t)uload(p.table + (min(t, p.end - 1) >> a.page_shift));
+}
+template <int ROWB>
+__device__ __forceinline__ size_t kv_locate(const KvAttention& a, const KvPart& p, uint32_t entry, int t)
+{
+    const size_t head = (size_t)ROWB << a.page_shift;
+    const uint32_t page = min(entry, (uint32_t)a.npages - 1), off = (uint32_t)(min(t, p.end - 1) & ~15) & ((1u << a.page_shift) - 1);
+    return wave_uniform(((size_t)page * a.Hkv + p.hkv) * head + (size_t)off * ROWB);
+}
+
+// The rows of one wave: RB blocks of 16, their softmax state and outputs, and 32 tokens' values.
+template <int IO, bool FP8, int D, int RB>
+struct KvRows {
+    using G = KvGeom<FP8, D>;
+    static constexpr int KS = G::KS, JN = G::JN, VE = G::VE, VL = G::VL, VW = G::VW;
+    static constexpr float OFF = IO == KV_F16 ? 10.f : 0.f;   // fp16 weights stay clear of its subnormals
+
+    float m[RB], l[RB];
+    f32x4 O[RB][JN];
+    int lim_hi[RB], lim_lo[RB];              // visible positions of the lane's row
+    uint32_t vf[2][4][VL][VW];               // values of tokens 16 blk + 4 (lane / 16) + r
+
+    __device__ __forceinline__ void init()
+    {
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb) {
             m[rb] = -INFINITY;
@@ -243,332 +312,256 @@ __global__ __launch_bounds__(256, OCC) void kv_attention_kernel(KvAttention a)
 #pragma unroll
             for (int j = 0; j < JN; ++j) O[rb][j] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
+    }
 
-        // ---- tokens
-        const int step = NTW * KV_SUB;
-        const int t_first = rng.base + ta * KV_TILE + tw * KV_SUB;
-        const int all_hi = end - a.T + 1;                                       // every row sees [all_lo, all_hi)
-        const int all_lo = a.window > 0 ? max(0, end - a.window) : 0;
-        const size_t head_bytes = ((size_t)D << a.page_shift) * EB;             // one head's part of a page
-        const uint8_t* Kc = static_cast<const uint8_t*>(a.K) + hkv * head_bytes;
-        const uint8_t* Vc = static_cast<const uint8_t*>(a.V) + hkv * head_bytes;
-        const size_t page_bytes = head_bytes * a.Hkv;
-        const uint32_t koff = n * D * EB + g * 16;                                  // token n, 16 bytes g
-        const uint32_t voff = g * 4 * D * EB + n * VE * EB;                         // tokens 4 g.., channels VE n..
-
-        u32x4 kf[2][KL];
-        uint32_t vf[2][4][VL][VW];
-        // Page and byte offset in the cache of the 16 tokens at t.  The page number is held inside the
-        // cache whatever the table says; positions whose entry is wrong are masked below.
-        auto page_of = [&](int t) { return (uint32_t)uload(table + (min(t, end - 1) >> a.page_shift)); };
-        auto locate = [&](uint32_t entry, int t) {
-            const int at = min(t, end - 1);
-            const uint32_t page = min(entry, (uint32_t)a.npages - 1);
-            return wave_uniform(page * page_bytes + (size_t)((at & ~15) & ((1 << a.page_shift) - 1)) * (D * EB));
-        };
-        auto load_k = [&](size_t b0, size_t b1) {
-#pragma unroll
-            for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-                for (int i = 0; i < KL; ++i)
-                    kf[blk][i] = kv_load<RW == 1, u32x4>(Kc + (blk ? b1 : b0) + i * 64 + koff);
-        };
-        auto load_v = [&](size_t b0, size_t b1) {
-#pragma unroll
-            for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-#pragma unroll
-                    for (int v = 0; v < VL; ++v) {
-                        const uint8_t* p = Vc + (blk ? b1 : b0) + (r * D * EB + v * 16 * VE * EB) + voff;
-                        if constexpr (VW == 4) {
-                            const u32x4 w = kv_load<RW == 1, u32x4>(p);
-                            vf[blk][r][v][0] = w.x;
-                            vf[blk][r][v][1] = w.y;
-                            vf[blk][r][v][2] = w.z;
-                            vf[blk][r][v][3] = w.w;
-                        } else if constexpr (VW == 2) {
-                            const u32x2 w = kv_load<RW == 1, u32x2>(p);
-                            vf[blk][r][v][0] = w.x;
-                            vf[blk][r][v][1] = w.y;
-                        } else {
-                            vf[blk][r][v][0] = kv_load<RW == 1, uint32_t>(p);
-                        }
-                    }
-        };
-        // scores of the 32 tokens in kf (raw products)
-        auto scores = [&](f32x4 (&s)[RB][2]) {
-            asm volatile("" ::: "memory");       // queries stay in LDS from block to block
-#pragma unroll
-            for (int rb = 0; rb < RB; ++rb) s[rb][0] = s[rb][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < KS; ++i) {
-                u32x4 qf[RB];
-#pragma unroll
-                for (int rb = 0; rb < RB; ++rb) qf[rb] = sh.q[wv][rb * KS + i][lane];
-#pragma unroll
-                for (int blk = 0; blk < 2; ++blk) {
-                    u32x4 A;
-                    if constexpr (FP8) {
-                        const u32x4 w = kf[blk][i >> 1];
-                        const uint32_t w0 = (i & 1) ? w.z : w.x, w1 = (i & 1) ? w.w : w.y;
-                        A = u32x4{kv_from_e4m3<IO, false>(w0), kv_from_e4m3<IO, true>(w0),
-                                  kv_from_e4m3<IO, false>(w1), kv_from_e4m3<IO, true>(w1)};
-                    } else {
-                        A = kf[blk][i];
-                    }
-#pragma unroll
-                    for (int rb = 0; rb < RB; ++rb) s[rb][blk] = kv_mfma<IO>(A, qf[rb], s[rb][blk]);
-                }
-            }
-        };
-        // Scores to weights (hi + lo), with the running reference, sum and outputs kept in step.
-        // see: which of the lane's eight tokens row block rb's row sees.
-        auto weights = [&](f32x4 (&s)[RB][2], const uint32_t (&see)[RB], auto masked, u32x4 (&ph)[RB], u32x4 (&pl)[RB]) {
-#pragma unroll
-            for (int rb = 0; rb < RB; ++rb) {
-                float top = -INFINITY;
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    top = fmaxf(top, !decltype(masked)::value || (see[rb] >> e & 1) ? s[rb][e >> 2][e & 3] : -INFINITY);
-                top *= sc_abs;
-                if (__builtin_amdgcn_ballot_w64(top > m[rb] + (OFF + KV_SLACK)) != 0) {
-                    // the row's maximum over the 32 tokens; its four lanes agree on the reference
-                    const float mx = max_over_row_groups(top);
-                    const float mn = mx > m[rb] + (OFF + KV_SLACK) ? mx - OFF : m[rb];
-                    const float f = mn == m[rb] ? 1.f : __builtin_amdgcn_exp2f(m[rb] - mn);
-                    m[rb] = mn;
-                    l[rb] *= f;
-#pragma unroll
-                    for (int j = 0; j < JN; ++j) O[rb][j] *= f;
-                }
-                const float ref = m[rb] == -INFINITY ? 0.f : m[rb];
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float p[2];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int e = 2 * i + k;
-                        // one rounding between the score and its exponent
-                        p[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[rb][e >> 2][e & 3], sc_abs, -ref));
-                        if constexpr (decltype(masked)::value) p[k] = (see[rb] >> e & 1) ? p[k] : 0.f;
-                        l[rb] += p[k];
-                    }
-                    kv_split<IO>(p[0], p[1], hi[i], lo[i]);
-                }
-                ph[rb] = u32x4{hi[0], hi[1], hi[2], hi[3]};
-                pl[rb] = u32x4{lo[0], lo[1], lo[2], lo[3]};
-            }
-        };
-        // O += V^T P^T for the wave's 32 tokens, of all rows or of those in mine
-        auto outputs = [&](const u32x4 (&ph)[RB], const u32x4 (&pl)[RB], auto some, const bool (&mine)[RB]) {
-            auto add = [&](u32x4 A, int j) {
-#pragma unroll
-                for (int rb = 0; rb < RB; ++rb) {
-                    const f32x4 x = kv_mfma<IO>(A, pl[rb], kv_mfma<IO>(A, ph[rb], O[rb][j]));
-                    if constexpr (decltype(some)::value) O[rb][j] = mine[rb] ? x : O[rb][j];
-                    else O[rb][j] = x;
-                }
-                if constexpr (decltype(some)::value) __builtin_amdgcn_sched_barrier(0);
-            };
-#pragma unroll
-            for (int v = 0; v < VL; ++v) {
-                if constexpr (FP8) {
-#pragma unroll
-                    for (int w = 0; w < VW; ++w) {
-                        // four channels of eight tokens: bytes of two tokens side by side, then widened
-                        uint32_t e[4][4];
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            const uint32_t x = vf[t >> 1][(t & 1) * 2][v][w], y = vf[t >> 1][(t & 1) * 2 + 1][v][w];
-                            const uint32_t c01 = __builtin_amdgcn_perm(y, x, 0x05010400u);
-                            const uint32_t c23 = __builtin_amdgcn_perm(y, x, 0x07030602u);
-                            e[0][t] = kv_from_e4m3<IO, false>(c01);
-                            e[1][t] = kv_from_e4m3<IO, true>(c01);
-                            e[2][t] = kv_from_e4m3<IO, false>(c23);
-                            e[3][t] = kv_from_e4m3<IO, true>(c23);
-                        }
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            add(u32x4{e[c][0], e[c][1], e[c][2], e[c][3]}, v * VE + w * 4 + c);
-                    }
-                } else {
-#pragma unroll
-                    for (int c = 0; c < VE; ++c) {
-                        const uint32_t sel = (c & 1) ? 0x07060302u : 0x05040100u;
-                        const int w = c >> 1;
-                        const u32x4 A = {__builtin_amdgcn_perm(vf[0][1][v][w], vf[0][0][v][w], sel),
-                                         __builtin_amdgcn_perm(vf[0][3][v][w], vf[0][2][v][w], sel),
-                                         __builtin_amdgcn_perm(vf[1][1][v][w], vf[1][0][v][w], sel),
-                                         __builtin_amdgcn_perm(vf[1][3][v][w], vf[1][2][v][w], sel)};
-                        add(A, v * VE + c);
-                    }
-                }
-            }
-        };
-
-        // ---- the first block's keys and values are requested before anything is waited for
-        const int nb = t_first < tend ? (tend - t_first + step - 1) / step : 0;     // the wave's blocks
-        int t0 = t_first;
-        uint32_t p0 = 0, p1 = 0, c0 = 0, c1 = 0;     // table entries of the next and of the current block
-        size_t b0 = 0, b1 = 0;
-        if (nb > 0) {
-            c0 = page_of(t0);
-            c1 = page_of(t0 + 16);
-            b0 = locate(c0, t0);
-            b1 = locate(c1, t0 + 16);
-            load_k(b0, b1);
-            load_v(b0, b1);
-            p0 = page_of(t0 + step);
-            p1 = page_of(t0 + step + 16);
-        }
-
-        // ---- queries: row n of each of the wave's blocks, eight channels of each product.  Each wave
-        // keeps its own copy in LDS; the barrier keeps it behind the previous range's join.
-        __syncthreads();
+    // Row limits, and the rows' queries in operand order to LDS: row block first + rb of the chunk.
+    __device__ __forceinline__ void queries(const KvAttention& a, const KvPart& p, int first, u32x4 (*dst)[64], int lane)
+    {
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb) {
-            const int nn = kv_opaque(lane & 15), row = chunk * a.rpc + (rg * RB + rb) * 16 + nn;
-            const int t = row / a.group, h = hkv * a.group + row - t * a.group;
-            const bool real = row < a.rows && (rg * RB + rb) * 16 + nn < a.rpc;
-            lim_hi[rb] = real ? end - a.T + t + 1 : end;
+            const int n = kv_opaque(lane & 15), g = lane >> 4, rl = (first + rb) * 16 + n, row = p.chunk * a.rpc + rl;
+            const int t = row / a.group, h = p.hkv * a.group + row - t * a.group;
+            const bool real = row < a.rows && rl < a.rpc;
+            lim_hi[rb] = real ? p.end - a.T + t + 1 : p.end;
             lim_lo[rb] = real && a.window > 0 ? max(0, lim_hi[rb] - a.window) : 0;
-            const uint16_t* q = static_cast<const uint16_t*>(a.q) + ((size_t)t * a.B + b) * a.q_stride + (size_t)h * D;
-            const uint32_t flip = sc < 0.f ? 0x80008000u : 0u;      // scores are scaled by |sc|
+            const uint16_t* q = static_cast<const uint16_t*>(a.q) + ((size_t)t * a.B + p.b) * a.q_stride + (size_t)h * D;
+            const uint32_t flip = p.sc < 0.f ? 0x80008000u : 0u;      // scores are scaled by |sc|
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
-                // the channels of K's loads: eight at a time, or halves of sixteen codes
+                // the channels of K's pieces: eight at a time, or halves of sixteen codes
                 const int d = FP8 ? (i >> 1) * 64 + g * 16 + (i & 1) * 8 : i * 32 + g * 8;
                 u32x4 w = real ? *reinterpret_cast<const u32x4*>(q + d) : u32x4{0, 0, 0, 0};
                 w ^= u32x4{flip, flip, flip, flip};
-                sh.q[wv][rb * KS + i][lane] = w;
+                dst[rb * KS + i][lane] = w;
             }
         }
-        // a table entry outside the cache sends the whole range through the masked path
-        bool wrong = false;
-        for (int i = ((rng.base + ta * KV_TILE) >> a.page_shift) + lane;
-             i < (tend + (1 << a.page_shift) - 1) >> a.page_shift; i += 64)
-            wrong |= (uint32_t)table[i] >= (uint32_t)a.npages;
-        wrong = __builtin_amdgcn_ballot_w64(wrong) != 0;
-        if (wrong && lane == 0 && a.err) atomicOr(a.err, KVERR_BAD_SLOT);
+    }
 
-        // ---- tokens.  Every block but the last requests the next one unconditionally: the waits for K
-        // and V then count exactly the requests behind them.
-        auto block = [&](auto more) {
-            f32x4 s[RB][2];
-            scores(s);
-            const int cur = t0;
-            const size_t cb0 = b0, cb1 = b1;
-            const bool ok0 = c0 < (uint32_t)a.npages, ok1 = c1 < (uint32_t)a.npages;
-            if constexpr (decltype(more)::value) {
-                t0 += step;
-                c0 = p0;
-                c1 = p1;
-                b0 = locate(c0, t0);
-                b1 = locate(c1, t0 + 16);
-                load_k(b0, b1);
-                p0 = page_of(t0 + step);
-                p1 = page_of(t0 + step + 16);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            u32x4 ph[RB], pl[RB];
-            uint32_t see[RB] = {};
-            bool mine[RB] = {};
-            if (!wrong && cur >= all_lo && cur + KV_SUB <= all_hi) {        // every row sees every token
-                weights(s, see, std::false_type{}, ph, pl);
-                outputs(ph, pl, std::false_type{}, mine);
-            } else {
-                const int mt = cur + 4 * kv_opaque(g);                      // the lane's first token
+    // Raw scores of 32 tokens; kf(blk, piece) gives 16 bytes of K, q the queries in LDS.
+    // FENCE: operands of at most that many products along the head are read ahead (registers).
+    template <int FENCE, typename KF>
+    __device__ __forceinline__ void scores(f32x4 (&s)[RB][2], const u32x4 (*q)[64], int lane, KF kf) const
+    {
 #pragma unroll
-                for (int rb = 0; rb < RB; ++rb) {
+        for (int rb = 0; rb < RB; ++rb) s[rb][0] = s[rb][1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int t = mt + (e >> 2) * 16 + (e & 3);
-                        if (t < lim_hi[rb] && t >= lim_lo[rb] && (e < 4 ? ok0 : ok1)) see[rb] |= 1u << e;
-                    }
-                }
-                weights(s, see, std::true_type{}, ph, pl);
-                // Values that no row sees count as zero, so that 0 * NaN does not arise.  A value that only
-                // some drafts see and that is no number would still reach the others: then, and only then,
-                // the drafts are taken one by one.
-                auto clear = [&](int lo, int hi) {
-                    uint32_t odd = 0;
+        for (int i = 0; i < KS; ++i) {
+            u32x4 qf[RB];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int t = mt + (e >> 2) * 16 + (e & 3);
-                        const bool sees = t < hi && t >= lo && (e < 4 ? ok0 : ok1);
-                        const bool some = t < all_lo || t >= all_hi;
+            for (int rb = 0; rb < RB; ++rb) qf[rb] = q[rb * KS + i][lane];
 #pragma unroll
-                        for (int v = 0; v < VL; ++v)
-#pragma unroll
-                            for (int w = 0; w < VW; ++w) {
-                                const uint32_t x = sees ? vf[e >> 2][e & 3][v][w] : 0u;
-                                vf[e >> 2][e & 3][v][w] = x;
-                                if (some) odd |= kv_odd<IO, FP8>(x);
-                            }
-                    }
-                    return __builtin_amdgcn_ballot_w64(odd != 0) != 0;
-                };
-                const bool odd = clear(a.window > 0 ? max(0, end - a.T + 1 - a.window) : 0, end);
-                if (a.T == 1 || !odd) {
-                    outputs(ph, pl, std::false_type{}, mine);
+            for (int blk = 0; blk < 2; ++blk) {
+                u32x4 A;
+                if constexpr (FP8) {
+                    const u32x4 w = kf(blk, i >> 1);
+                    const uint32_t w0 = (i & 1) ? w.z : w.x, w1 = (i & 1) ? w.w : w.y;
+                    A = u32x4{kv_from_e4m3<IO, false>(w0), kv_from_e4m3<IO, true>(w0),
+                              kv_from_e4m3<IO, false>(w1), kv_from_e4m3<IO, true>(w1)};
                 } else {
-#pragma unroll 1
-                    for (int d = 0; d < a.T; ++d) {
-                        const int hi = end - a.T + d + 1;
-                        load_v(cb0, cb1);
-                        clear(a.window > 0 ? max(0, hi - a.window) : 0, hi);
+                    A = kf(blk, i);
+                }
 #pragma unroll
-                        for (int rb = 0; rb < RB; ++rb) mine[rb] = lim_hi[rb] == hi;
-                        outputs(ph, pl, std::true_type{}, mine);
+                for (int rb = 0; rb < RB; ++rb) s[rb][blk] = kv_mfma<IO>(A, qf[rb], s[rb][blk]);
+            }
+            if (FENCE > 0 && (i + 1) % (FENCE > 0 ? FENCE : 1) == 0) __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+
+    // Scores to weights (hi + lo), with the running reference, sum and outputs kept in step; a masked
+    // score is -inf.
+    __device__ __forceinline__ void weights(const f32x4 (&s)[RB][2], float sc, u32x4 (&ph)[RB], u32x4 (&pl)[RB])
+    {
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) {
+            float top = s[rb][0][0];
+#pragma unroll
+            for (int e = 1; e < 8; ++e) top = fmaxf(top, s[rb][e >> 2][e & 3]);
+            top *= sc;
+            if (__builtin_amdgcn_ballot_w64(top > m[rb] + (OFF + KV_SLACK)) != 0) {
+                // the row's maximum over the 32 tokens; its four lanes agree on the reference
+                const float mx = max_over_row_groups(top);
+                const float mn = mx > m[rb] + (OFF + KV_SLACK) ? mx - OFF : m[rb];
+                const float f = mn == m[rb] ? 1.f : __builtin_amdgcn_exp2f(m[rb] - mn);
+                m[rb] = mn;
+                l[rb] *= f;
+#pragma unroll
+                for (int j = 0; j < JN; ++j) O[rb][j] *= f;
+            }
+            const float ref = m[rb] == -INFINITY ? 0.f : m[rb];
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float w[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int e = 2 * i + k;
+                    // one rounding between the score and its exponent
+                    w[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[rb][e >> 2][e & 3], sc, -ref));
+                    l[rb] += w[k];
+                }
+                kv_split<IO>(w[0], w[1], hi[i], lo[i]);
+            }
+            ph[rb] = u32x4{hi[0], hi[1], hi[2], hi[3]};
+            pl[rb] = u32x4{lo[0], lo[1], lo[2], lo[3]};
+        }
+    }
+
+    // O += V^T P^T for the 32 tokens in vf, of all rows or of those in mine.
+    template <bool SOME>
+    __device__ __forceinline__ void outputs(const u32x4 (&ph)[RB], const u32x4 (&pl)[RB], const bool (&mine)[RB])
+    {
+        auto add = [&](u32x4 A, int j) {
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb) {
+                const f32x4 x = kv_mfma<IO>(A, pl[rb], kv_mfma<IO>(A, ph[rb], O[rb][j]));
+                if constexpr (SOME) O[rb][j] = mine[rb] ? x : O[rb][j];
+                else O[rb][j] = x;
+            }
+            if constexpr (SOME) __builtin_amdgcn_sched_barrier(0);
+        };
+#pragma unroll
+        for (int v = 0; v < VL; ++v) {
+            if constexpr (FP8) {
+#pragma unroll
+                for (int w = 0; w < VW; ++w) {
+                    // four channels of eight tokens: bytes of two tokens side by side, then widened
+                    uint32_t e[4][4];
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const uint32_t x = vf[t >> 1][(t & 1) * 2][v][w], y = vf[t >> 1][(t & 1) * 2 + 1][v][w];
+                        const uint32_t c01 = __builtin_amdgcn_perm(y, x, 0x05010400u);
+                        const uint32_t c23 = __builtin_amdgcn_perm(y, x, 0x07030602u);
+                        e[0][t] = kv_from_e4m3<IO, false>(c01);
+                        e[1][t] = kv_from_e4m3<IO, true>(c01);
+                        e[2][t] = kv_from_e4m3<IO, false>(c23);
+                        e[3][t] = kv_from_e4m3<IO, true>(c23);
                     }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) add(u32x4{e[c][0], e[c][1], e[c][2], e[c][3]}, v * VE + w * 4 + c);
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < VE; ++c) {
+                    const uint32_t sel = (c & 1) ? 0x07060302u : 0x05040100u;
+                    const int w = c >> 1;
+                    add(u32x4{__builtin_amdgcn_perm(vf[0][1][v][w], vf[0][0][v][w], sel),
+                              __builtin_amdgcn_perm(vf[0][3][v][w], vf[0][2][v][w], sel),
+                              __builtin_amdgcn_perm(vf[1][1][v][w], vf[1][0][v][w], sel),
+                              __builtin_amdgcn_perm(vf[1][3][v][w], vf[1][2][v][w], sel)}, v * VE + c);
                 }
             }
-            if constexpr (decltype(more)::value) {
-                load_v(b0, b1);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        };
-        if (nb > 0) {
-#pragma unroll 1
-            for (int left = nb - 1; left > 0; --left) block(std::true_type{});
-            block(std::false_type{});
         }
+    }
 
-        // ---- join the waves of each row group; whole ranges write the output
-        const bool whole = ta == 0 && tb == rng.tiles;
-        const int slot = 2 * blockIdx.x + (ta == 0 ? 1 : 0);
-        const float vs = FP8 ? uload(a.v_scale + hkv) : 1.f;
-        const int jt = kv_opaque(tid), jn = jt & 15, jg = (jt >> 4) & 3;
+    // Values outside [lo, hi) or of a wrong page become zero; true if some position that not every
+    // row sees holds no number.  mt: the lane's first token.
+    __device__ __forceinline__ bool clear(const KvPart& p, int mt, int lo, int hi, bool ok0, bool ok1)
+    {
+        uint32_t odd = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int t = mt + (e >> 2) * 16 + (e & 3);
+            const bool sees = t < hi && t >= lo && (e < 4 ? ok0 : ok1), some = t < p.all_lo || t >= p.all_hi;
+#pragma unroll
+            for (int v = 0; v < VL; ++v)
+#pragma unroll
+                for (int w = 0; w < VW; ++w) {
+                    const uint32_t x = sees ? vf[e >> 2][e & 3][v][w] : 0u;
+                    vf[e >> 2][e & 3][v][w] = x;
+                    if (some) odd |= kv_odd<IO, FP8>(x);
+                }
+        }
+        return __builtin_amdgcn_ballot_w64(odd != 0) != 0;
+    }
+
+    // 32 tokens that every row sees, whose raw scores are s: weights and outputs.  values() fills vf.
+    template <typename VF>
+    __device__ __forceinline__ void take(const KvPart& p, const f32x4 (&s)[RB][2], VF values)
+    {
+        u32x4 ph[RB], pl[RB];
+        const bool mine[RB] = {};
+        weights(s, p.sc_abs(), ph, pl);
+        values();
+        outputs<false>(ph, pl, mine);
+    }
+
+    // The 32 tokens at t0, whoever sees them.  ok0, ok1: the two blocks' pages are in the cache.
+    // values(again) fills vf.
+    template <typename VF>
+    __device__ __forceinline__ void take_masked(const KvAttention& a, const KvPart& p, f32x4 (&s)[RB][2], int t0, bool ok0,
+                                                bool ok1, int lane, VF values)
+    {
+        const int mt = t0 + 4 * kv_opaque(lane >> 4);                            // the lane's first token
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int t = mt + (e >> 2) * 16 + (e & 3);
+                const bool sees = t < lim_hi[rb] && t >= lim_lo[rb] && (e < 4 ? ok0 : ok1);
+                s[rb][e >> 2][e & 3] = sees ? s[rb][e >> 2][e & 3] : -INFINITY;
+            }
+        u32x4 ph[RB], pl[RB];
+        weights(s, p.sc_abs(), ph, pl);
+        // Values that no row sees count as zero, so that 0 * NaN does not arise.  A value that only some
+        // drafts see and that is no number would still reach the others: then, and only then, the drafts
+        // are taken one by one.
+        bool apart = false;
+#pragma unroll 1
+        for (int d = -1; d < (apart ? a.T : 0); ++d) {
+            const int hi = d < 0 ? p.end : p.all_hi + d;
+            const int lo = a.window > 0 ? max(0, (d < 0 ? p.all_hi : hi) - a.window) : 0;
+            values(d >= 0);
+            const bool odd = clear(p, mt, lo, hi, ok0, ok1);
+            if (d < 0) {
+                apart = a.T > 1 && odd;
+                if (apart) continue;
+            }
+            bool mine[RB];
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb) mine[rb] = d < 0 || lim_hi[rb] == hi;
+            outputs<true>(ph, pl, mine);
+        }
+    }
+
+    // Joins the NTW waves (wave = tw * RW + rg) that split a row group's tokens, JP 16-channel groups
+    // at a time through so [waves][16][16 JP + 4]; a whole range writes its output, a part its partial rows.
+    template <int NT, int RW, int NTW, int JP>
+    __device__ __forceinline__ void join(const KvAttention& a, const KvPart& p, float (*so)[16][16 * JP + 4],
+                                         float (*s_m)[16], float (*s_l)[16])
+    {
+        const bool whole = p.whole();
+        const int slot = 2 * blockIdx.x + (p.ta == 0 ? 1 : 0);
+        const float vs = FP8 ? uload(a.v_scale + p.hkv) : 1.f;
+        const int jt = kv_opaque(threadIdx.x), jn = jt & 15, jg = (jt >> 4) & 3, wv = uni(threadIdx.x >> 6);
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb) {
             const float lw = sum_over_row_groups(l[rb]);
 #pragma unroll
             for (int jp = 0; jp < JN; jp += JP) {
-                __syncthreads();                                 // queries or the previous part are done with
+                __syncthreads();                                 // the queries, blocks or part before are done with
                 if (jp == 0 && jg == 0) {
                     s_m[wv][jn] = m[rb];
                     s_l[wv][jn] = lw;
                 }
-                // lane: row n, channels VE (4 g + r).. of each load's 16 VE
+                // lane: row n, channels VE (4 g + r).. of each piece's 16 VE; a round takes whole pieces,
+                // or JP channels of every lane's VE
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
 #pragma unroll
                     for (int j = 0; j < JP; j += 4) {
                         const int jj = jp + j, d = (jj / VE) * 16 * VE + (4 * jg + r) * VE + jj % VE;
-                        // channel within the joined 16 JP: whole loads of 16 VE, or the halves of one
                         const int c = VE <= JP ? d - jp * 16 : (4 * jg + r) * JP + j;
-                        st4(&s_o[wv][jn][c], f32x4{O[rb][jj][r], O[rb][jj + 1][r], O[rb][jj + 2][r], O[rb][jj + 3][r]});
+                        st4(&so[wv][jn][c], f32x4{O[rb][jj][r], O[rb][jj + 1][r], O[rb][jj + 2][r], O[rb][jj + 3][r]});
                     }
                 __syncthreads();
-                constexpr int C8 = JP * 2;                       // eight-channel pieces of a row
-                for (int i = jt; i < RW * 16 * C8; i += 256) {
-                    const int rr = i / C8, c = (i - rr * C8) * 8, grp = rr >> 4, nn = rr & 15;
-                    const int rl = (grp * RB + rb) * 16 + nn, row = chunk * a.rpc + rl;
+                // four channels at a time where a lane's run is no longer, else eight
+                constexpr int CW = VE > JP && JP < 8 ? 4 : 8, C8 = 16 * JP / CW;
+                for (int i = jt; i < RW * 16 * C8; i += NT) {
+                    const int rr = i / C8, c = (i - rr * C8) * CW, grp = rr >> 4, nn = rr & 15;
+                    const int rl = (grp * RB + rb) * 16 + nn, row = p.chunk * a.rpc + rl;
                     if (rl >= a.rpc || row >= a.rows) continue;
-                    const int d = VE <= JP ? jp * 16 + c : (c / JP) * VE + jp + c % JP;
-                    float M = -INFINITY, L = 0.f, x[8] = {};
+                    const int d = VE <= JP ? jp * 16 + c : (c / JP) * VE + (jp / VE) * 16 * VE + jp % VE + c % JP;
+                    float M = -INFINITY, L = 0.f, x[CW] = {};
 #pragma unroll
                     for (int k = 0; k < NTW; ++k) M = fmaxf(M, s_m[k * RW + grp][nn]);
 #pragma unroll
@@ -576,23 +569,24 @@ __global__ __launch_bounds__(256, OCC) void kv_attention_kernel(KvAttention a)
                         const float mk = s_m[k * RW + grp][nn];
                         const float f = mk == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(mk - M);
                         L += f * s_l[k * RW + grp][nn];
-                        const f32x4 y0 = ld4(&s_o[k * RW + grp][nn][c]), y1 = ld4(&s_o[k * RW + grp][nn][c + 4]);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            x[e] += f * y0[e];
-                            x[4 + e] += f * y1[e];
+                        for (int e = 0; e < CW; e += 4) {
+                            const f32x4 y = ld4(&so[k * RW + grp][nn][c + e]);
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) x[e + z] += f * y[z];
                         }
                     }
                     if (whole) {
                         const float inv = L == 0.f ? 0.f : vs / L;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] *= inv;
-                        kv_store_o<IO>(a, b, hkv, row, d, D, x);
-                        if (d == 0) kv_store_lse(a, b, hkv, row, M, L);
+                        for (int e = 0; e < CW; ++e) x[e] *= inv;
+                        kv_store_o<IO>(a, p.b, p.hkv, row, d, D, x);
+                        if (d == 0) kv_store_lse(a, p.b, p.hkv, row, M, L);
                     } else {
                         const size_t at = (size_t)slot * a.rpc + rl;
-                        st4(a.part_o + at * D + d, f32x4{x[0], x[1], x[2], x[3]});
-                        st4(a.part_o + at * D + d + 4, f32x4{x[4], x[5], x[6], x[7]});
+#pragma unroll
+                        for (int e = 0; e < CW; e += 4)
+                            st4(a.part_o + at * D + d + e, f32x4{x[e], x[e + 1], x[e + 2], x[e + 3]});
                         if (d == 0) {
                             a.part_ml[2 * at] = M;
                             a.part_ml[2 * at + 1] = L;
@@ -601,13 +595,266 @@ __global__ __launch_bounds__(256, OCC) void kv_attention_kernel(KvAttention a)
                 }
             }
         }
-        if (tid == 0 && ta == 0 && (by_range || !whole)) {
-            const int range = b * hc + seg;
-            int32_t* mt = a.meta + 2 * (by_range ? range : (int)blockIdx.x);
-            mt[0] = by_range ? (whole ? -1 : (int)blockIdx.x) : range;
-            mt[1] = cut.owner(pre + (seg + 1) * rng.tiles - 1);
+    }
+};
+
+// After a part: the note for kv_combine_kernel, and on to the next part.
+__device__ __forceinline__ void kv_next(const KvAttention& a, const KvPart& p, const int* s_pre, KvLine& ln)
+{
+    const bool whole = p.whole();
+    if (threadIdx.x == 0 && p.ta == 0 && (ln.by_range || !whole)) {
+        const int range = p.b * ln.hc + p.seg;
+        int32_t* mt = a.meta + 2 * (ln.by_range ? range : (int)blockIdx.x);
+        mt[0] = ln.by_range ? (whole ? -1 : (int)blockIdx.x) : range;
+        mt[1] = ln.cut.owner(s_pre[p.b] + (p.seg + 1) * p.tiles - 1);
+    }
+    ln.u += p.tb - p.ta;
+}
+
+// Up to 16 RB rows share a key/value head: four waves split its tokens, each with K and V straight
+// in registers.  Shared memory: prefix sums [B + 1] (dynamic).
+template <int IO, bool FP8, int D, int RB, int OCC>
+__global__ __launch_bounds__(256, OCC) void kv_attention_kernel(KvAttention a)
+{
+    using G = KvGeom<FP8, D>;
+    using R = KvRows<IO, FP8, D, RB>;
+    constexpr int JP = G::JN < 8 ? G::JN : 8, EB = G::EB, VE = G::VE, VL = G::VL, VW = G::VW, KL = G::KL;
+    extern __shared__ int s_pre[];
+    // the waves' queries while tokens pass, their outputs when they are joined
+    __shared__ union alignas(16) {
+        u32x4 q[4][RB * G::KS][64];
+        float o[4][16][16 * JP + 4];
+    } sh;
+    __shared__ float s_m[4][16], s_l[4][16];
+    __shared__ int s_wave[4];
+    const int lane = threadIdx.x & 63, wv = uni(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
+    KvLine ln;
+    if (!kv_line<256>(a, s_pre, s_wave, ln)) return;
+#pragma unroll 1
+    while (ln.u < ln.u1) {
+        const KvPart p = kv_part<FP8>(a, s_pre, ln);
+        R rows;
+        rows.init();
+        constexpr int step = 4 * KV_SUB;
+        const int t_first = p.base + p.ta * KV_TILE + wv * KV_SUB;
+        const uint8_t* Kc = static_cast<const uint8_t*>(a.K);
+        const uint8_t* Vc = static_cast<const uint8_t*>(a.V);
+        const uint32_t koff = n * G::ROWB + g * 16;                             // token n, 16 bytes g
+        const uint32_t voff = g * 4 * G::ROWB + n * VE * EB;                    // tokens 4 g.., channels VE n..
+        u32x4 kf[2][KL];
+        auto load_k = [&](size_t b0, size_t b1) {
+#pragma unroll
+            for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+                for (int i = 0; i < KL; ++i) kf[blk][i] = kv_stream<u32x4>(Kc + (blk ? b1 : b0) + i * 64 + koff);
+        };
+        auto load_v = [&](size_t b0, size_t b1) {
+#pragma unroll
+            for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int v = 0; v < VL; ++v)
+                        kv_words<VW, true>(Vc + (blk ? b1 : b0) + (r * G::ROWB + v * 16 * VE * EB) + voff, rows.vf[blk][r][v]);
+        };
+        // the first block's keys and values are requested before anything is waited for
+        const int nb = t_first < p.tend ? (p.tend - t_first + step - 1) / step : 0;     // the wave's blocks
+        int t0 = t_first;
+        uint32_t p0 = 0, p1 = 0, c0 = 0, c1 = 0;     // table entries of the next and of the current block
+        size_t b0 = 0, b1 = 0;
+        if (nb > 0) {
+            c0 = kv_page_of(a, p, t0);
+            c1 = kv_page_of(a, p, t0 + 16);
+            b0 = kv_locate<G::ROWB>(a, p, c0, t0);
+            b1 = kv_locate<G::ROWB>(a, p, c1, t0 + 16);
+            load_k(b0, b1);
+            load_v(b0, b1);
+            p0 = kv_page_of(a, p, t0 + step);
+            p1 = kv_page_of(a, p, t0 + step + 16);
         }
-        u += tb - ta;
+        __syncthreads();                             // the join before is done with sh
+        rows.queries(a, p, 0, sh.q[wv], lane);       // each wave keeps its own copy
+        const bool wrong = kv_wrong_pages(a, p, lane);
+
+        // Every block but the last requests the next one unconditionally: the waits for K and V then
+        // count exactly the requests behind them.  Blocks that every row sees have a loop of their own
+        // (its registers stay clear of the masks'); the last block goes the masked way whatever it is.
+        int left = nb - 1;
+        auto next_k = [&] {
+            t0 += step;
+            c0 = p0;
+            c1 = p1;
+            b0 = kv_locate<G::ROWB>(a, p, c0, t0);
+            b1 = kv_locate<G::ROWB>(a, p, c1, t0 + 16);
+            load_k(b0, b1);
+            p0 = kv_page_of(a, p, t0 + step);
+            p1 = kv_page_of(a, p, t0 + step + 16);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        auto next_v = [&] {
+            load_v(b0, b1);
+            --left;
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        auto scores = [&](f32x4 (&s)[RB][2]) {
+            asm volatile("" ::: "memory");           // queries stay in LDS from block to block
+            rows.template scores<0>(s, sh.q[wv], lane, [&](int blk, int i) { return kf[blk][i]; });
+        };
+        auto masked = [&](auto more) {
+            f32x4 s[RB][2];
+            scores(s);
+            const int cur = t0;
+            const size_t cb0 = b0, cb1 = b1;
+            const bool ok0 = c0 < (uint32_t)a.npages, ok1 = c1 < (uint32_t)a.npages;
+            if constexpr (decltype(more)::value) next_k();
+            rows.take_masked(a, p, s, cur, ok0, ok1, lane, [&](bool again) {
+                if (again) load_v(cb0, cb1);
+            });
+            if constexpr (decltype(more)::value) next_v();
+        };
+        while (left > 0) {
+#pragma unroll 1
+            while (left > 0 && (wrong || !p.full(t0, KV_SUB))) masked(std::true_type{});
+#pragma unroll 1
+            while (left > 0 && !wrong && p.full(t0, KV_SUB)) {
+                f32x4 s[RB][2];
+                scores(s);
+                next_k();
+                rows.take(p, s, [] {});
+                next_v();
+            }
+        }
+        if (left == 0) masked(std::false_type{});
+        rows.template join<256, 1, 4, JP>(a, p, sh.o, s_m, s_l);
+        kv_next(a, p, s_pre, ln);
+    }
+}
+
+// More rows: eight waves in four row groups of 16 RB rows, two waves of a group splitting its
+// tokens.  The cache passes through LDS in stages of ST tokens, so that it is read once for all
+// rows: each wave requests its eighth of the next stage into registers, and writes it to LDS when
+// the workgroup is through with the stage before.  K's 16-byte pieces are permuted within a token
+// (fold) so that 16 tokens' equal pieces lie in different banks.
+template <int IO, bool FP8, int D, int RB>
+__global__ __launch_bounds__(512, 1) void kv_attention_wide_kernel(KvAttention a)
+{
+    using G = KvGeom<FP8, D>;
+    using R = KvRows<IO, FP8, D, RB>;
+    constexpr int RW = 4, NTW = 2, EB = G::EB, VE = G::VE, VL = G::VL, VW = G::VW, ROWB = G::ROWB;
+    constexpr int ST = ROWB <= 256 ? KV_TILE : KV_TILE / 2;      // tokens of a stage
+    constexpr int CPB = 16 * ROWB / 1024;                        // 1 KiB chunks of 16 tokens
+    constexpr int NC = ST / 16 * CPB;                            // chunks of K, and of V
+    constexpr int CJ = NC / 8;                                   // of them a wave's
+    constexpr int TPC = 1024 / ROWB;                             // tokens of a chunk
+    constexpr int FT = ROWB >= 256 ? 1 : 256 / ROWB, FM = ROWB / 16 < 16 ? ROWB / 16 - 1 : 15;
+    constexpr int JP = 4;
+    static_assert(NC % 8 == 0 && 8 % CPB == 0, "every wave takes whole chunks");
+    extern __shared__ int s_pre[];
+    __shared__ union alignas(16) {
+        uint8_t kv[2][ST * ROWB];                                // a stage of K and of V
+        float o[8][16][16 * JP + 4];
+    } sh;
+    __shared__ u32x4 s_q[RW][RB * G::KS][64];
+    __shared__ float s_m[8][16], s_l[8][16];
+    __shared__ int s_wave[8];
+    const int lane = threadIdx.x & 63, wv = uni(threadIdx.x >> 6), rg = wv % RW, tw = wv / RW, n = lane & 15, g = lane >> 4;
+    KvLine ln;
+    if (!kv_line<512>(a, s_pre, s_wave, ln)) return;
+    // a wave's chunks are the same part of blocks wv / CPB, wv / CPB + 8 / CPB, ..; the lane's bytes there
+    const int part = wv % CPB, blk0 = wv / CPB, tok = part * TPC + lane * 16 / ROWB, pos = lane * 16 % ROWB / 16;
+    const uint32_t voff = part * 1024 + lane * 16;
+    const uint32_t koff = tok * ROWB + (pos ^ ((tok / FT) & FM)) * 16;
+#pragma unroll 1
+    while (ln.u < ln.u1) {
+        const KvPart p = kv_part<FP8>(a, s_pre, ln);
+        R rows;
+        rows.init();
+        const uint8_t* Kc = static_cast<const uint8_t*>(a.K);
+        const uint8_t* Vc = static_cast<const uint8_t*>(a.V);
+        const int first = uni(p.base + p.ta * KV_TILE), ns = uni(first < p.tend ? (p.tend - first + ST - 1) / ST : 0);
+        u32x4 kr[CJ], vr[CJ];                                    // the wave's chunks of the next stage
+        uint32_t entry[CJ];                                      // and the pages of those after it
+        auto pages = [&](int st) {
+#pragma unroll
+            for (int j = 0; j < CJ; ++j) entry[j] = kv_page_of(a, p, st + 16 * (blk0 + j * (8 / CPB)));
+        };
+        auto request = [&](int st) {
+#pragma unroll
+            for (int j = 0; j < CJ; ++j) {
+                const size_t at = kv_locate<ROWB>(a, p, entry[j], st + 16 * (blk0 + j * (8 / CPB)));
+                kr[j] = kv_stream<u32x4>(Kc + at + koff);
+                vr[j] = kv_stream<u32x4>(Vc + at + voff);
+            }
+            pages(st + ST);
+        };
+        if (ns > 0) {
+            pages(first);
+            request(first);
+        }
+        __syncthreads();                                         // the join before is done with LDS
+        rows.queries(a, p, rg * RB, s_q[rg], lane);              // (two waves write the same)
+        const bool wrong = kv_wrong_pages(a, p, lane);
+        int st = first;
+        const int st_end = first + ns * ST;
+        auto turn = [&] {                                        // the requested stage to LDS, the next one requested
+            __syncthreads();                                     // the stage before is used up
+#pragma unroll
+            for (int j = 0; j < CJ; ++j) {
+                const int c = wv + 8 * j;
+                *reinterpret_cast<u32x4*>(sh.kv[0] + c * 1024 + lane * 16) = kr[j];
+                *reinterpret_cast<u32x4*>(sh.kv[1] + c * 1024 + lane * 16) = vr[j];
+            }
+            if (st + ST < st_end) request(st + ST);
+            __syncthreads();
+        };
+        const int fold = (n / FT) & FM;
+        auto scores = [&](f32x4 (&s)[RB][2], int sb) {
+            const uint8_t* ks = sh.kv[0] + (sb * KV_SUB + n) * ROWB;
+            rows.template scores<2>(s, s_q[rg], lane, [&](int blk, int i) {
+                return *reinterpret_cast<const u32x4*>(ks + blk * 16 * ROWB + ((i * 4 + g) ^ fold) * 16);
+            });
+            __builtin_amdgcn_sched_barrier(0);                   // V is read when K is used up
+        };
+        auto values = [&](int sb) {
+            const uint8_t* vs = sh.kv[1] + (sb * KV_SUB + 4 * g) * ROWB + n * VE * EB;
+#pragma unroll
+            for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int v = 0; v < VL; ++v)
+                        kv_words<VW, false>(vs + (blk * 16 + r) * ROWB + v * 16 * VE * EB, rows.vf[blk][r][v]);
+        };
+        while (st < st_end) {
+#pragma unroll 1
+            while (st < st_end && (wrong || !p.full(st, ST))) {
+                turn();
+                const int nsb = uni(min(ST, p.tend - st + KV_SUB - 1) / KV_SUB);
+#pragma unroll 1
+                for (int sb = tw; sb < nsb; sb += NTW) {
+                    const int t0 = st + sb * KV_SUB;
+                    f32x4 s[RB][2];
+                    scores(s, sb);
+                    const bool ok0 = kv_page_of(a, p, t0) < (uint32_t)a.npages;
+                    const bool ok1 = kv_page_of(a, p, t0 + 16) < (uint32_t)a.npages;
+                    rows.take_masked(a, p, s, t0, ok0, ok1, lane, [&](bool) { values(sb); });
+                }
+                st += ST;
+            }
+#pragma unroll 1
+            while (st < st_end && !wrong && p.full(st, ST)) {    // every row sees every token
+                turn();
+#pragma unroll 1
+                for (int sb = tw; sb < ST / KV_SUB; sb += NTW) {
+                    f32x4 s[RB][2];
+                    scores(s, sb);
+                    rows.take(p, s, [&] { values(sb); });
+                }
+                st += ST;
+            }
+        }
+        rows.template join<512, RW, NTW, JP>(a, p, sh.o, s_m, s_l);
+        kv_next(a, p, s_pre, ln);
     }
 }
 
@@ -671,10 +918,21 @@ __global__ __launch_bounds__(256) void kv_combine_kernel(KvAttention a)
     }
 }
 
-template <int IO, bool FP8, int D, int RB, int RW, int OCC>
-static hipError_t kv_attention_start(const KvAttention& a, const KvPlan& p, hipStream_t s)
+template <int IO, bool FP8, int D>
+static hipError_t kv_attention_width(const KvAttention& a, const KvPlan& p, hipStream_t s)
 {
-    hipLaunchKernelGGL((kv_attention_kernel<IO, FP8, D, RB, RW, OCC>), dim3(p.nwg), dim3(256), (a.B + 1) * sizeof(int), s, a);
+    const size_t lds = (a.B + 1) * sizeof(int);
+    const dim3 grid(p.nwg);
+    if (p.wide) {
+        if constexpr (D < 256) {
+            if (p.RB == 2) hipLaunchKernelGGL((kv_attention_wide_kernel<IO, FP8, D, 2>), grid, dim3(512), lds, s, a);
+        }
+        if (p.RB == 1) hipLaunchKernelGGL((kv_attention_wide_kernel<IO, FP8, D, 1>), grid, dim3(512), lds, s, a);
+    } else if (p.RB == 2) {
+        hipLaunchKernelGGL((kv_attention_kernel<IO, FP8, D, 2, kv_occ(D, FP8, 2)>), grid, dim3(256), lds, s, a);
+    } else {
+        hipLaunchKernelGGL((kv_attention_kernel<IO, FP8, D, 1, kv_occ(D, FP8, 1)>), grid, dim3(256), lds, s, a);
+    }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int ranges = a.B * a.Hkv * a.nchunk, most = ranges <= p.nwg ? ranges : p.nwg;
@@ -687,21 +945,10 @@ static hipError_t kv_attention_start(const KvAttention& a, const KvPlan& p, hipS
 template <int IO, bool FP8>
 static hipError_t kv_attention_pick(const KvAttention& a, const KvPlan& p, int D, hipStream_t s)
 {
-    // (row blocks per wave, row groups) of kv_attention_plan, and the workgroups a CU is cut for
-    const int k = D * 100 + p.RB * 10 + p.RW;
-    constexpr bool F = FP8;
-    switch (k) {
-        case 6411: return kv_attention_start<IO, F, 64, 1, 1, kv_occ(64, F, 1)>(a, p, s);
-        case 6421: return kv_attention_start<IO, F, 64, 2, 1, kv_occ(64, F, 2)>(a, p, s);
-        case 6422: return kv_attention_start<IO, F, 64, 2, 2, kv_occ(64, F, 2)>(a, p, s);
-        case 6424: return kv_attention_start<IO, F, 64, 2, 4, kv_occ(64, F, 2)>(a, p, s);
-        case 12811: return kv_attention_start<IO, F, 128, 1, 1, kv_occ(128, F, 1)>(a, p, s);
-        case 12821: return kv_attention_start<IO, F, 128, 2, 1, kv_occ(128, F, 2)>(a, p, s);
-        case 12822: return kv_attention_start<IO, F, 128, 2, 2, kv_occ(128, F, 2)>(a, p, s);
-        case 12824: return kv_attention_start<IO, F, 128, 2, 4, kv_occ(128, F, 2)>(a, p, s);
-        case 25611: return kv_attention_start<IO, F, 256, 1, 1, kv_occ(256, F, 1)>(a, p, s);
-        case 25612: return kv_attention_start<IO, F, 256, 1, 2, kv_occ(256, F, 1)>(a, p, s);
-        case 25614: return kv_attention_start<IO, F, 256, 1, 4, kv_occ(256, F, 1)>(a, p, s);
+    switch (D) {
+        case 64: return kv_attention_width<IO, FP8, 64>(a, p, s);
+        case 128: return kv_attention_width<IO, FP8, 128>(a, p, s);
+        case 256: return kv_attention_width<IO, FP8, 256>(a, p, s);
         default: return hipErrorInvalidValue;
     }
 }
