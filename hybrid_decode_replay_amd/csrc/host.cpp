@@ -23,13 +23,22 @@ KvPlan kv_attention_plan(int D, bool fp8, int rows)
 {
     KvPlan p;
     p.wide = rows > 32;
-    const int block = p.wide ? 64 : 16;
-    p.RB = rows <= block || (p.wide && D == 256) ? 1 : 2;
-    const int most = block * p.RB;
+    p.RB = rows <= 16 || (p.wide && D == 256) ? 1 : 2;
+    p.RW = p.wide ? (rows > 64 || D == 256 ? 4 : 2) : 1;
+    const int most = 16 * p.RB * p.RW;
     p.rpc = rows < most ? rows : most;
     p.nchunk = (rows + most - 1) / most;
     p.nwg = 256 * (p.wide ? 1 : kv_occ(D, fp8, p.RB));
     return p;
+}
+
+// Splitting evens the work out but costs a second launch and the partial rows (about 12 us); a
+// workgroup per range costs the wait for the longest one.  Measured: drafts in a window of 1024 tokens
+// 34 us split, 19 whole; 2048 ranges of up to 2001 tokens 126 and 114; 512 ranges of up to 4097 tokens
+// 120 and 142.
+bool kv_attention_whole(long long tokens, long long ranges)
+{
+    return ranges < (1 << 22) && (tokens <= 1280 || (tokens <= 2560 && ranges >= 2048));
 }
 
 }  // namespace rs
@@ -1362,6 +1371,9 @@ replay_status replay_kv_attention(const replay_kv_layer* layer, const replay_kv_
     a.rows = x.ntok * a.group;
     a.rpc = p.rpc;
     a.nchunk = p.nchunk;
+    // the most tokens a sequence's rows can see, in blocks of 32
+    const long long cap = (long long)x.max_pages * layer->page_size, seen = (long long)a.window + x.ntok - 1 + 31;
+    a.whole = rs::kv_attention_whole(a.window > 0 && seen < cap ? seen : cap, (long long)x.batch * Hkv * p.nchunk);
     a.scale_log2 = (float)((double)x.scale * 1.4426950408889634);
     const bool bf = layer->io_dtype == REPLAY_BF16, fp8 = layer->cache_dtype == REPLAY_FP8_E4M3;
     const auto run = bf ? (fp8 ? rs::launch_kv_attention_bf16_fp8 : rs::launch_kv_attention_bf16)

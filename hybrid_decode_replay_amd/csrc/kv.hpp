@@ -56,14 +56,15 @@ struct KvAttention {
     float* part_o;           // [2 nwg][rpc][D]
     int B, Hq, Hkv, group, T, npages, page_shift, max_pages, window;
     int rows;                // T * group rows share a key/value head
-    int rpc;                 // rows of a chunk, at most 16 RB (64 RB in the wide kernel)
+    int rpc;                 // rows of a chunk, at most 16 RB RW
     int nchunk;              // chunks of rows
+    bool whole;              // a workgroup per range, nothing to join
     float scale_log2;        // scale * log2(e)
 };
-// How a call is cut: row blocks of 16 per wave, the kernel for many rows or for few, rows of a
-// chunk, chunks, workgroups.  The rule stands at kv_attention_plan.
+// How a call is cut: row blocks of 16 per wave, row groups (more than one in the wide kernel), rows
+// of a chunk, chunks, workgroups.  The rule stands at kv_attention_plan.
 struct KvPlan {
-    int RB;
+    int RB, RW;
     bool wide;
     int rpc, nchunk, nwg;
 };
@@ -75,6 +76,8 @@ constexpr int kv_occ(int D, bool fp8, int RB)
     return D == 256 || (D == 128 && RB == 2 && !fp8) ? 1 : 2;
 }
 KvPlan kv_attention_plan(int D, bool fp8, int rows);
+// Whether ranges of at most `tokens` tokens are short enough for a workgroup each.
+bool kv_attention_whole(long long tokens, long long ranges);
 // One translation unit per io and cache type.
 hipError_t launch_kv_attention_bf16(const KvAttention& a, const KvPlan& p, int D, hipStream_t s);
 hipError_t launch_kv_attention_bf16_fp8(const KvAttention& a, const KvPlan& p, int D, hipStream_t s);

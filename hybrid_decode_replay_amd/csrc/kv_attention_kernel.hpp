@@ -41,7 +41,6 @@ namespace rs {
 constexpr int KV_TILE = 128;                 // tokens of a work unit
 constexpr int KV_SUB = 32;                   // tokens a wave takes at once
 constexpr float KV_SLACK = 5.f;              // powers of two a weight may pass its reference by
-constexpr int KV_MAX_WG = 1024;              // workgroups of a call
 
 // x, but not to the compiler: what is computed from it stays where it is written, instead of
 // being carried in registers through the token loop.
@@ -240,19 +239,17 @@ struct KvPart {
     // every row sees every one of the n tokens at t
     __device__ __forceinline__ bool full(int t, int n) const { return t >= all_lo && t + n <= all_hi; }
 };
+// Tiles [ta, tb) of range seg (head and row chunk) of sequence b.  Everything goes to scalar
+// registers: the loops over tokens then branch without masks.
 template <bool FP8>
-__device__ __forceinline__ KvPart kv_part(const KvAttention& a, const int* s_pre, KvLine& ln)
+__device__ __forceinline__ KvPart kv_part(const KvAttention& a, int b, const KvRange& rng, int seg, int ta, int tb)
 {
     KvPart p;
-    while (uni(s_pre[ln.b + 1]) <= ln.u) ++ln.b;
-    // everything to scalar registers: the loops over tokens then branch without masks
-    p.b = uni(ln.b);
-    const KvRange rng = kv_range(a, uload(a.end + p.b), true);
-    const int at = ln.u - uni(s_pre[p.b]);
+    p.b = uni(b);
     p.tiles = uni(rng.tiles);
-    p.seg = uni(at / p.tiles);
-    p.ta = uni(at - p.seg * p.tiles);
-    p.tb = uni(min(p.tiles, p.ta + ln.u1 - ln.u));
+    p.seg = uni(seg);
+    p.ta = uni(ta);
+    p.tb = uni(tb);
     p.hkv = uni(p.seg / a.nchunk);
     p.chunk = uni(p.seg - p.hkv * a.nchunk);
     p.end = uni(rng.end);
@@ -263,6 +260,28 @@ __device__ __forceinline__ KvPart kv_part(const KvAttention& a, const int* s_pre
     p.table = a.table + (size_t)p.b * a.max_pages;
     p.sc = FP8 ? a.scale_log2 * uload(a.k_scale + p.hkv) : a.scale_log2;
     return p;
+}
+// The next part of a workgroup's stretch of the line.
+template <bool FP8>
+__device__ __forceinline__ KvPart kv_line_part(const KvAttention& a, const int* s_pre, KvLine& ln)
+{
+    while (uni(s_pre[ln.b + 1]) <= ln.u) ++ln.b;
+    const int b = uni(ln.b), at = ln.u - uni(s_pre[b]);
+    const KvRange rng = kv_range(a, uload(a.end + b), true);
+    const int seg = at / rng.tiles, ta = at - seg * rng.tiles;
+    return kv_part<FP8>(a, b, rng, seg, ta, min(rng.tiles, ta + ln.u1 - ln.u));
+}
+// Range blockIdx.x as one part (calls without a line); false for an idle sequence.
+template <bool FP8>
+__device__ __forceinline__ bool kv_whole_part(const KvAttention& a, KvPart& p)
+{
+    const int hc = a.Hkv * a.nchunk, b = uni(blockIdx.x / hc), seg = uni(blockIdx.x - b * hc);
+    if (a.active && !uload(a.active + b)) return false;
+    const int e = uload(a.end + b);
+    if (seg == 0 && threadIdx.x == 0 && a.err && (e < 0 || e > (a.max_pages << a.page_shift))) atomicOr(a.err, KVERR_BAD_SLOT);
+    const KvRange rng = kv_range(a, e, true);
+    p = kv_part<FP8>(a, b, rng, seg, 0, rng.tiles);
+    return true;
 }
 
 // Whether a table entry of the part lies outside the cache (its blocks then take the masked path).
@@ -453,25 +472,34 @@ struct KvRows {
         }
     }
 
-    // Values outside [lo, hi) or of a wrong page become zero; true if some position that not every
-    // row sees holds no number.  mt: the lane's first token.
-    __device__ __forceinline__ bool clear(const KvPart& p, int mt, int lo, int hi, bool ok0, bool ok1)
+    // Values outside [lo, hi) or of a wrong page become zero.  mt: the lane's first token.
+    __device__ __forceinline__ void clear(int mt, int lo, int hi, bool ok0, bool ok1)
     {
-        uint32_t odd = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const int t = mt + (e >> 2) * 16 + (e & 3);
-            const bool sees = t < hi && t >= lo && (e < 4 ? ok0 : ok1), some = t < p.all_lo || t >= p.all_hi;
+            const bool sees = t < hi && t >= lo && (e < 4 ? ok0 : ok1);
 #pragma unroll
             for (int v = 0; v < VL; ++v)
 #pragma unroll
-                for (int w = 0; w < VW; ++w) {
-                    const uint32_t x = sees ? vf[e >> 2][e & 3][v][w] : 0u;
-                    vf[e >> 2][e & 3][v][w] = x;
-                    if (some) odd |= kv_odd<IO, FP8>(x);
-                }
+                for (int w = 0; w < VW; ++w) vf[e >> 2][e & 3][v][w] = sees ? vf[e >> 2][e & 3][v][w] : 0u;
         }
-        return __builtin_amdgcn_ballot_w64(odd != 0) != 0;
+    }
+    // Whether some position that not every row sees holds no number.
+    __device__ __forceinline__ bool odd(const KvPart& p, int mt) const
+    {
+        uint32_t x = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int t = mt + (e >> 2) * 16 + (e & 3);
+            uint32_t y = 0;
+#pragma unroll
+            for (int v = 0; v < VL; ++v)
+#pragma unroll
+                for (int w = 0; w < VW; ++w) y |= kv_odd<IO, FP8>(vf[e >> 2][e & 3][v][w]);
+            x |= t < p.all_lo || t >= p.all_hi ? y : 0u;
+        }
+        return __builtin_amdgcn_ballot_w64(x != 0) != 0;
     }
 
     // 32 tokens that every row sees, whose raw scores are s: weights and outputs.  values() fills vf.
@@ -509,12 +537,11 @@ struct KvRows {
 #pragma unroll 1
         for (int d = -1; d < (apart ? a.T : 0); ++d) {
             const int hi = d < 0 ? p.end : p.all_hi + d;
-            const int lo = a.window > 0 ? max(0, (d < 0 ? p.all_hi : hi) - a.window) : 0;
             values(d >= 0);
-            const bool odd = clear(p, mt, lo, hi, ok0, ok1);
-            if (d < 0) {
-                apart = a.T > 1 && odd;
-                if (apart) continue;
+            clear(mt, a.window > 0 ? max(0, (d < 0 ? p.all_hi : hi) - a.window) : 0, hi, ok0, ok1);
+            if (d < 0 && a.T > 1 && odd(p, mt)) {
+                apart = true;
+                continue;
             }
             bool mine[RB];
 #pragma unroll
@@ -629,10 +656,11 @@ __global__ __launch_bounds__(256, OCC) void kv_attention_kernel(KvAttention a)
     __shared__ int s_wave[4];
     const int lane = threadIdx.x & 63, wv = uni(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
     KvLine ln;
-    if (!kv_line<256>(a, s_pre, s_wave, ln)) return;
+    KvPart p;
+    if (a.whole ? !kv_whole_part<FP8>(a, p) : !kv_line<256>(a, s_pre, s_wave, ln)) return;
 #pragma unroll 1
-    while (ln.u < ln.u1) {
-        const KvPart p = kv_part<FP8>(a, s_pre, ln);
+    while (a.whole || ln.u < ln.u1) {
+        if (!a.whole) p = kv_line_part<FP8>(a, s_pre, ln);
         R rows;
         rows.init();
         constexpr int step = 4 * KV_SUB;
@@ -678,7 +706,7 @@ __global__ __launch_bounds__(256, OCC) void kv_attention_kernel(KvAttention a)
 
         // Every block but the last requests the next one unconditionally: the waits for K and V then
         // count exactly the requests behind them.  Blocks that every row sees have a loop of their own
-        // (its registers stay clear of the masks'); the last block goes the masked way whatever it is.
+        // (its registers stay clear of the masks').
         int left = nb - 1;
         auto next_k = [&] {
             t0 += step;
@@ -724,23 +752,34 @@ __global__ __launch_bounds__(256, OCC) void kv_attention_kernel(KvAttention a)
                 next_v();
             }
         }
-        if (left == 0) masked(std::false_type{});
+        if (left == 0) {
+            bool taken = false;
+            if constexpr (D * RB < 512) {            // (more registers of outputs are not held twice)
+                if ((taken = !wrong && p.full(t0, KV_SUB))) {
+                    f32x4 s[RB][2];
+                    scores(s);
+                    rows.take(p, s, [] {});
+                }
+            }
+            if (!taken) masked(std::false_type{});
+        }
         rows.template join<256, 1, 4, JP>(a, p, sh.o, s_m, s_l);
+        if (a.whole) break;
         kv_next(a, p, s_pre, ln);
     }
 }
 
-// More rows: eight waves in four row groups of 16 RB rows, two waves of a group splitting its
+// More rows: eight waves in RW row groups of 16 RB rows, the 8 / RW waves of a group splitting its
 // tokens.  The cache passes through LDS in stages of ST tokens, so that it is read once for all
 // rows: each wave requests its eighth of the next stage into registers, and writes it to LDS when
 // the workgroup is through with the stage before.  K's 16-byte pieces are permuted within a token
 // (fold) so that 16 tokens' equal pieces lie in different banks.
-template <int IO, bool FP8, int D, int RB>
+template <int IO, bool FP8, int D, int RB, int RW>
 __global__ __launch_bounds__(512, 1) void kv_attention_wide_kernel(KvAttention a)
 {
     using G = KvGeom<FP8, D>;
     using R = KvRows<IO, FP8, D, RB>;
-    constexpr int RW = 4, NTW = 2, EB = G::EB, VE = G::VE, VL = G::VL, VW = G::VW, ROWB = G::ROWB;
+    constexpr int NTW = 8 / RW, EB = G::EB, VE = G::VE, VL = G::VL, VW = G::VW, ROWB = G::ROWB;
     constexpr int ST = ROWB <= 256 ? KV_TILE : KV_TILE / 2;      // tokens of a stage
     constexpr int CPB = 16 * ROWB / 1024;                        // 1 KiB chunks of 16 tokens
     constexpr int NC = ST / 16 * CPB;                            // chunks of K, and of V
@@ -759,14 +798,15 @@ __global__ __launch_bounds__(512, 1) void kv_attention_wide_kernel(KvAttention a
     __shared__ int s_wave[8];
     const int lane = threadIdx.x & 63, wv = uni(threadIdx.x >> 6), rg = wv % RW, tw = wv / RW, n = lane & 15, g = lane >> 4;
     KvLine ln;
-    if (!kv_line<512>(a, s_pre, s_wave, ln)) return;
+    KvPart p;
+    if (a.whole ? !kv_whole_part<FP8>(a, p) : !kv_line<512>(a, s_pre, s_wave, ln)) return;
     // a wave's chunks are the same part of blocks wv / CPB, wv / CPB + 8 / CPB, ..; the lane's bytes there
     const int part = wv % CPB, blk0 = wv / CPB, tok = part * TPC + lane * 16 / ROWB, pos = lane * 16 % ROWB / 16;
     const uint32_t voff = part * 1024 + lane * 16;
     const uint32_t koff = tok * ROWB + (pos ^ ((tok / FT) & FM)) * 16;
 #pragma unroll 1
-    while (ln.u < ln.u1) {
-        const KvPart p = kv_part<FP8>(a, s_pre, ln);
+    while (a.whole || ln.u < ln.u1) {
+        if (!a.whole) p = kv_line_part<FP8>(a, s_pre, ln);
         R rows;
         rows.init();
         const uint8_t* Kc = static_cast<const uint8_t*>(a.K);
@@ -854,24 +894,25 @@ __global__ __launch_bounds__(512, 1) void kv_attention_wide_kernel(KvAttention a
             }
         }
         rows.template join<512, RW, NTW, JP>(a, p, sh.o, s_m, s_l);
+        if (a.whole) break;
         kv_next(a, p, s_pre, ln);
     }
 }
 
 // Joins the partial rows of one split range, a row at a time.  blockIdx.x is the range where there
-// are no more of them than workgroups, else the workgroup that opened it.  The parts' references and sums first, each part's weight into LDS, then the outputs by 256
+// are no more of them than workgroups, else the workgroup that opened it.  256
 // threads = D / 4 lanes of four channels x 1024 / D groups of parts.
 template <int IO, bool FP8, int D, bool BY_RANGE>
 __global__ __launch_bounds__(256) void kv_combine_kernel(KvAttention a)
 {
     constexpr int CL = D / 4, PG = 256 / CL;
-    __shared__ float s_x[PG][D], s_w[KV_MAX_WG], s_m[4], s_l[4];
+    __shared__ float s_x[PG][D], s_m[PG], s_l[PG];
     const int hc = a.Hkv * a.nchunk, found = uload(a.meta + 2 * blockIdx.x);
     const int range = BY_RANGE ? blockIdx.x : found, w0 = BY_RANGE ? found : blockIdx.x;
     const int b = max(range, 0) / hc, seg = range - b * hc;
     if ((BY_RANGE && a.active && !uload(a.active + b)) || found < 0) return;
     const int w1 = uload(a.meta + 2 * blockIdx.x + 1);
-    const int np = w1 - w0 + 1, tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+    const int np = w1 - w0 + 1, tid = threadIdx.x;
     const int hkv = seg / a.nchunk, chunk = seg - hkv * a.nchunk;
     const int c = tid % CL, pg = tid / CL;
     const float vs = FP8 ? uload(a.v_scale + hkv) : 1.f;
@@ -880,39 +921,56 @@ __global__ __launch_bounds__(256) void kv_combine_kernel(KvAttention a)
     auto part = [&](int i, int rl) { return (size_t)(2 * (w0 + i) + (i == 0 ? 1 : 0)) * a.rpc + rl; };
     for (int rl = blockIdx.y; rl < rows; rl += gridDim.y) {
         float M = -INFINITY, L = 0.f;
-        for (int i = tid; i < np; i += 256) M = fmaxf(M, a.part_ml[2 * part(i, rl)]);
-#pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor(M, o, 64));
-        if (lane == 0) s_m[wv] = M;
-        __syncthreads();
-        M = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-        for (int i = tid; i < np; i += 256) {
-            const float m = a.part_ml[2 * part(i, rl)];
-            const float f = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - M);
-            s_w[i] = f;
-            L += f * a.part_ml[2 * part(i, rl) + 1];
-        }
-        L = wave_sum64(L);
-        if (lane == 0) s_l[wv] = L;
-        __syncthreads();
         f32x4 x = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-        for (int i = pg; i < np; i += PG) x += ld4(a.part_o + part(i, rl) * D + 4 * c) * s_w[i];
+        // eight parts at a time, all of their loads on the way together
+        for (int i0 = pg; i0 < np; i0 += 8 * PG) {
+            float m[8], l[8];
+            f32x4 y[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const size_t at = part(min(i0 + k * PG, np - 1), rl);
+                m[k] = a.part_ml[2 * at];
+                l[k] = a.part_ml[2 * at + 1];
+                y[k] = ld4(a.part_o + at * D + 4 * c);
+            }
+            float mx = M;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) mx = fmaxf(mx, m[k]);
+            const float f0 = M == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(M - mx);
+            M = mx;
+            L *= f0;
+            x *= f0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (i0 + k * PG >= np) continue;
+                const float f = m[k] == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[k] - M);
+                L += l[k] * f;
+                x += y[k] * f;
+            }
+        }
         st4(&s_x[pg][4 * c], x);
+        if (c == 0) {
+            s_m[pg] = M;
+            s_l[pg] = L;
+        }
         __syncthreads();
         if (tid < D / 8) {
-            L = s_l[0] + s_l[1] + s_l[2] + s_l[3];
-            float y[8] = {};
+            float MM = -INFINITY, LL = 0.f, y[8] = {};
 #pragma unroll
-            for (int k = 0; k < PG; ++k)
+            for (int k = 0; k < PG; ++k) MM = fmaxf(MM, s_m[k]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] += s_x[k][8 * tid + e];
-            const float inv = L == 0.f ? 0.f : vs / L;
+            for (int k = 0; k < PG; ++k) {
+                const float f = s_m[k] == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(s_m[k] - MM);
+                LL += s_l[k] * f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] += s_x[k][8 * tid + e] * f;
+            }
+            const float inv = LL == 0.f ? 0.f : vs / LL;
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] *= inv;
             const int row = chunk * a.rpc + rl;
             kv_store_o<IO>(a, b, hkv, row, 8 * tid, D, y);
-            if (tid == 0) kv_store_lse(a, b, hkv, row, M, L);
+            if (tid == 0) kv_store_lse(a, b, hkv, row, MM, LL);
         }
         __syncthreads();
     }
@@ -921,21 +979,24 @@ __global__ __launch_bounds__(256) void kv_combine_kernel(KvAttention a)
 template <int IO, bool FP8, int D>
 static hipError_t kv_attention_width(const KvAttention& a, const KvPlan& p, hipStream_t s)
 {
-    const size_t lds = (a.B + 1) * sizeof(int);
-    const dim3 grid(p.nwg);
+    const int ranges = a.B * a.Hkv * a.nchunk;
+    const size_t lds = a.whole ? 0 : (a.B + 1) * sizeof(int);
+    const dim3 grid(a.whole ? ranges : p.nwg);
     if (p.wide) {
-        if constexpr (D < 256) {
-            if (p.RB == 2) hipLaunchKernelGGL((kv_attention_wide_kernel<IO, FP8, D, 2>), grid, dim3(512), lds, s, a);
+        if constexpr (D == 256) {
+            hipLaunchKernelGGL((kv_attention_wide_kernel<IO, FP8, D, 1, 4>), grid, dim3(512), lds, s, a);
+        } else {
+            if (p.RW == 2) hipLaunchKernelGGL((kv_attention_wide_kernel<IO, FP8, D, 2, 2>), grid, dim3(512), lds, s, a);
+            else hipLaunchKernelGGL((kv_attention_wide_kernel<IO, FP8, D, 2, 4>), grid, dim3(512), lds, s, a);
         }
-        if (p.RB == 1) hipLaunchKernelGGL((kv_attention_wide_kernel<IO, FP8, D, 1>), grid, dim3(512), lds, s, a);
     } else if (p.RB == 2) {
         hipLaunchKernelGGL((kv_attention_kernel<IO, FP8, D, 2, kv_occ(D, FP8, 2)>), grid, dim3(256), lds, s, a);
     } else {
         hipLaunchKernelGGL((kv_attention_kernel<IO, FP8, D, 1, kv_occ(D, FP8, 1)>), grid, dim3(256), lds, s, a);
     }
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const int ranges = a.B * a.Hkv * a.nchunk, most = ranges <= p.nwg ? ranges : p.nwg;
+    if (e != hipSuccess || a.whole) return e;
+    const int most = ranges <= p.nwg ? ranges : p.nwg;
     const int y = p.rpc < 8192 / most ? p.rpc : 8192 / most;         // rows side by side, within some waves of the chip
     if (ranges <= p.nwg) hipLaunchKernelGGL((kv_combine_kernel<IO, FP8, D, true>), dim3(ranges, y), dim3(256), 0, s, a);
     else hipLaunchKernelGGL((kv_combine_kernel<IO, FP8, D, false>), dim3(p.nwg, y), dim3(256), 0, s, a);
