@@ -588,11 +588,15 @@ def kv_layer(nheads, nkv, head_dim, npages, page_size, io_dtype=BF16, cache_dtyp
                    npages, page_size, rot_dim, rot_style)
 
 
+_KV_DTYPES = {}
+
+
 def _kv_torch_dtypes(layer: KVLayer):
     """(io dtype, cache dtype) of a layer as torch dtypes."""
-    torch = _torch()
-    kinds = {BF16: torch.bfloat16, F16: torch.float16, FP8_E4M3: torch.float8_e4m3fn}
-    return kinds.get(layer.io_dtype), kinds.get(layer.cache_dtype)
+    if not _KV_DTYPES:
+        torch = _torch()
+        _KV_DTYPES.update({BF16: torch.bfloat16, F16: torch.float16, FP8_E4M3: torch.float8_e4m3fn})
+    return _KV_DTYPES.get(layer.io_dtype), _KV_DTYPES.get(layer.cache_dtype)
 
 
 def kv_cache(layer: KVLayer, device="cuda"):
@@ -605,47 +609,54 @@ def kv_cache(layer: KVLayer, device="cuda"):
     return one(), one()
 
 
-class _On:
-    """Makes a tensor's device the current one for a call, so that the launch goes to that
-    device's current stream, and checks that the call's other tensors are on it too."""
+# The paged cache's calls are small, and an eager decode step makes several per layer: each tensor is
+# checked by one expression, and its fault is looked for only when that fails.
+def _addr(t, device, dtype, name, shape=None):
+    """Address of a contiguous tensor on `device` (None stays None)."""
+    if t is None:
+        return None
+    if t.device != device or t.dtype != dtype or (shape is not None and t.shape != shape) or not t.is_contiguous():
+        _complain(t, device, dtype, name, shape)
+    return t.data_ptr()
 
-    def __init__(self, device):
-        torch = _torch()
-        if device.type != "cuda":
-            raise ValueError("the paged cache's tensors must be device tensors")
-        self.device = device
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self
+def _rows(t, device, dtype, name, rows, width):
+    """(address, row stride) of [rows][width] with contiguous rows."""
+    if t.device != device or t.dtype != dtype or t.shape != (rows, width):
+        _complain(t, device, dtype, name, (rows, width))
+    stride, one = t.stride()
+    if one != 1 and width > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), stride if rows > 1 else width
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
 
-    def ptr(self, t, dtype=None, name="tensor", shape=None):
-        """Address of a contiguous tensor (None stays None)."""
-        if t is None:
-            return None
-        if t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, expected {self.device}")
-        if shape is not None and tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        return _ptr(t, dtype, name).value
+def _complain(t, device, dtype, name, shape):
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
-    def rows(self, t, dtype, name, rows, width):
-        """(address, row stride) of [rows][width] with contiguous rows."""
-        if t.dim() != 2 or tuple(t.shape) != (rows, width):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, width)}")
-        if t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, expected {self.device}")
-        if t.dtype != dtype:
-            raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-        if width > 1 and t.stride(1) != 1:
-            raise ValueError(f"{name} must have contiguous rows")
-        return t.data_ptr(), t.stride(0) if rows > 1 else width
+
+def _on_device(device):
+    if device.type != "cuda":
+        raise ValueError("the paged cache's tensors must be device tensors")
+    return device
+
+
+def _launch(device, where, fn, *args):
+    """Calls fn(*args, stream) on the current stream of `device`, which is made the current device."""
+    torch = _torch()
+    index = device.index
+    if index == torch.cuda.current_device():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != OK:
+        raise ReplayError(status, where)
 
 
 class KVPages:
@@ -701,51 +712,47 @@ class KVPages:
     def free(self):
         return self._part(64 + 7 * self._bp + self.cfg.batch * self.cfg.max_pages, self.cfg.npages)
 
+    def _mem(self):
+        return ctypes.byref(self.cfg), _addr(self.mem, _on_device(self.device), _torch().int32, "mem")
+
     def reset(self):
-        with _On(self.device) as on:
-            _check(_lib.replay_kv_reset(ctypes.byref(self.cfg), on.ptr(self.mem), _stream()), "replay_kv_reset")
+        _launch(self.device, "replay_kv_reset", _lib.replay_kv_reset, *self._mem())
 
     def reserve(self, ntok=1, counts=None, active=None, rows=None, slots=None, pos=None, starts=None):
         """Pages for a step's new tokens: `ntok` each, rows [ntok][B], or `counts` (device int32 [B]),
         packed rows (`rows` of them in all, or as many as `slots` has).  Returns (slots, pos), with
         counts (slots, pos, starts)."""
         torch = _torch()
-        B = self.cfg.batch
-        with _On(self.device) as on:
-            if slots is not None:
-                rows = slots.numel() if rows is None else rows
-            elif rows is None:
-                if counts is not None:
-                    raise ValueError("counts need rows (or slots): how many rows the step's arrays have")
-                rows = ntok * B
-            if slots is None:
-                slots = torch.empty(rows, dtype=torch.int64, device=self.device)
-            if pos is None:
-                pos = torch.empty(rows, dtype=torch.int32, device=self.device)
+        B, dev = self.cfg.batch, self.device
+        if slots is not None:
+            rows = slots.numel() if rows is None else rows
+        elif rows is None:
             if counts is not None:
-                ntok = 0
-                if starts is None:
-                    starts = torch.empty(B + 1, dtype=torch.int32, device=self.device)
-            _check(_lib.replay_kv_reserve(
-                ctypes.byref(self.cfg), on.ptr(self.mem), int(ntok), on.ptr(counts, torch.int32, "counts", (B,)),
-                on.ptr(active, torch.uint8, "active", (B,)), int(rows), on.ptr(slots, torch.int64, "slots", (rows,)),
-                on.ptr(pos, torch.int32, "pos", (rows,)), on.ptr(starts, torch.int32, "starts", (B + 1,)), _stream()),
-                "replay_kv_reserve")
+                raise ValueError("counts need rows (or slots): how many rows the step's arrays have")
+            rows = ntok * B
+        if slots is None:
+            slots = torch.empty(rows, dtype=torch.int64, device=dev)
+        if pos is None:
+            pos = torch.empty(rows, dtype=torch.int32, device=dev)
+        if counts is not None:
+            ntok = 0
+            if starts is None:
+                starts = torch.empty(B + 1, dtype=torch.int32, device=dev)
+        _launch(dev, "replay_kv_reserve", _lib.replay_kv_reserve, *self._mem(), int(ntok),
+                _addr(counts, dev, torch.int32, "counts", (B,)), _addr(active, dev, torch.uint8, "active", (B,)),
+                int(rows), _addr(slots, dev, torch.int64, "slots", (rows,)), _addr(pos, dev, torch.int32, "pos", (rows,)),
+                _addr(starts, dev, torch.int32, "starts", (B + 1,)))
         return (slots, pos) if counts is None else (slots, pos, starts)
 
     def commit(self, accepted=None):
         """Keeps accepted[b] (device int32 [B], None = all) of the open step's tokens."""
-        with _On(self.device) as on:
-            _check(_lib.replay_kv_commit(ctypes.byref(self.cfg), on.ptr(self.mem),
-                                         on.ptr(accepted, _torch().int32, "accepted", (self.cfg.batch,)), _stream()),
-                   "replay_kv_commit")
+        _launch(self.device, "replay_kv_commit", _lib.replay_kv_commit, *self._mem(),
+                _addr(accepted, self.device, _torch().int32, "accepted", (self.cfg.batch,)))
 
     def release(self, mask=None):
         """Empties the sequences `mask` (device uint8 [B], None = all) marks; their pages are free again."""
-        with _On(self.device) as on:
-            _check(_lib.replay_kv_release(ctypes.byref(self.cfg), on.ptr(self.mem),
-                                          on.ptr(mask, _torch().uint8, "mask", (self.cfg.batch,)), _stream()),
-                   "replay_kv_release")
+        _launch(self.device, "replay_kv_release", _lib.replay_kv_release, *self._mem(),
+                _addr(mask, self.device, _torch().uint8, "mask", (self.cfg.batch,)))
 
 
 def kv_append(layer: KVLayer, K, V, k, v, slots, q=None, q_out=None, pos=None, freq=None, axis=None, k_scale=None,
@@ -755,33 +762,33 @@ def kv_append(layer: KVLayer, K, V, k, v, slots, q=None, q_out=None, pos=None, f
     freq fp32 [rot_dim/2], axis uint8 [rot_dim/2].  Returns q_out (None without q)."""
     torch = _torch()
     io, kind = _kv_torch_dtypes(layer)
-    n = k.shape[0]
-    shape = (layer.npages, layer.nkv, layer.page_size, layer.head_dim)
-    a = KVAppendArgs()
-    with _On(K.device) as on:
-        a.K, a.V = on.ptr(K, kind, "K", shape), on.ptr(V, kind, "V", shape)
-        a.rows = n
-        a.k, a.k_stride = on.rows(k, io, "k", n, layer.nkv * layer.head_dim)
-        a.v, a.v_stride = on.rows(v, io, "v", n, layer.nkv * layer.head_dim)
-        if q is not None:
-            a.q, a.q_stride = on.rows(q, io, "q", n, layer.nheads * layer.head_dim)
-            if q_out is None:
-                q_out = torch.zeros((n, layer.nheads * layer.head_dim), dtype=io, device=K.device)
-            a.q_out = on.ptr(q_out, io, "q_out", (n, layer.nheads * layer.head_dim))
-        elif q_out is not None:
-            raise ValueError("q_out without q")
-        a.slots = on.ptr(slots, torch.int64, "slots", (n,))
-        if layer.rot_dim > 0:
-            if pos is None or freq is None:
-                raise ValueError("a rotated layer needs pos and freq")
-            a.naxes = 1 if pos.dim() == 1 else pos.shape[0]
-            a.pos = on.ptr(pos, torch.int32, "pos", (n,) if pos.dim() == 1 else (a.naxes, n))
-            a.freq = on.ptr(freq, torch.float32, "freq", (layer.rot_dim // 2,))
-            a.axis = on.ptr(axis, torch.uint8, "axis", (layer.rot_dim // 2,))
-        a.k_scale = on.ptr(k_scale, torch.float32, "k_scale", (layer.nkv,))
-        a.v_scale = on.ptr(v_scale, torch.float32, "v_scale", (layer.nkv,))
-        a.err = on.ptr(err, torch.int32, "err", (1,))
-        _check(_lib.replay_kv_append(ctypes.byref(layer), ctypes.byref(a), _stream()), "replay_kv_append")
+    n, D, Hkv, dev = k.shape[0], layer.head_dim, layer.nkv, _on_device(K.device)
+    shape, width = (layer.npages, Hkv, layer.page_size, D), Hkv * D
+    a = KVAppendArgs(rows=n, K=_addr(K, dev, kind, "K", shape), V=_addr(V, dev, kind, "V", shape),
+                     slots=_addr(slots, dev, torch.int64, "slots", (n,)))
+    a.k, a.k_stride = _rows(k, dev, io, "k", n, width)
+    a.v, a.v_stride = _rows(v, dev, io, "v", n, width)
+    if q is not None:
+        width = layer.nheads * D
+        a.q, a.q_stride = _rows(q, dev, io, "q", n, width)
+        if q_out is None:
+            q_out = torch.zeros((n, width), dtype=io, device=dev)
+        a.q_out = _addr(q_out, dev, io, "q_out", (n, width))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if layer.rot_dim > 0:
+        if pos is None or freq is None:
+            raise ValueError("a rotated layer needs pos and freq")
+        a.naxes = 1 if pos.dim() == 1 else pos.shape[0]
+        a.pos = _addr(pos, dev, torch.int32, "pos", (n,) if pos.dim() == 1 else (a.naxes, n))
+        a.freq = _addr(freq, dev, torch.float32, "freq", (layer.rot_dim // 2,))
+        a.axis = _addr(axis, dev, torch.uint8, "axis", (layer.rot_dim // 2,))
+    if k_scale is not None or v_scale is not None:
+        a.k_scale = _addr(k_scale, dev, torch.float32, "k_scale", (Hkv,))
+        a.v_scale = _addr(v_scale, dev, torch.float32, "v_scale", (Hkv,))
+    if err is not None:
+        a.err = _addr(err, dev, torch.int32, "err", (1,))
+    _launch(dev, "replay_kv_append", _lib.replay_kv_append, ctypes.byref(layer), ctypes.byref(a))
     return q_out
 
 
@@ -797,31 +804,31 @@ def kv_attention(layer: KVLayer, q, K, V, table, end, ntok=1, scale=None, window
     uint8 tensor of kv_attention_workspace bytes; one is allocated for the call if None."""
     torch = _torch()
     io, kind = _kv_torch_dtypes(layer)
-    B = end.shape[0]
-    shape = (layer.npages, layer.nkv, layer.page_size, layer.head_dim)
-    a = KVAttentionArgs()
-    with _On(K.device) as on:
-        a.q, a.q_stride = on.rows(q, io, "q", ntok * B, layer.nheads * layer.head_dim)
-        a.K, a.V = on.ptr(K, kind, "K", shape), on.ptr(V, kind, "V", shape)
-        a.k_scale = on.ptr(k_scale, torch.float32, "k_scale", (layer.nkv,))
-        a.v_scale = on.ptr(v_scale, torch.float32, "v_scale", (layer.nkv,))
-        if table.dim() != 2:
-            raise ValueError("table must be [B][max_pages]")
-        a.table = on.ptr(table, torch.int32, "table", (B, table.shape[1]))
-        a.end = on.ptr(end, torch.int32, "end", (B,))
-        a.active = on.ptr(active, torch.uint8, "active", (B,))
-        a.batch, a.max_pages, a.ntok, a.window = B, table.shape[1], ntok, window
-        a.scale = layer.head_dim ** -0.5 if scale is None else scale
-        if o is None:
-            o = torch.zeros((ntok, B, layer.nheads, layer.head_dim), dtype=io, device=K.device)
-        a.o = on.ptr(o, io, "o", (ntok, B, layer.nheads, layer.head_dim))
-        a.lse = on.ptr(lse, torch.float32, "lse", (ntok, B, layer.nheads))
-        a.err = on.ptr(err, torch.int32, "err", (1,))
-        need = kv_attention_workspace(layer, B, ntok)
-        if ws is None:
-            ws = torch.empty(max(need, 1), dtype=torch.uint8, device=K.device)
-        _check(_lib.replay_kv_attention(ctypes.byref(layer), ctypes.byref(a), on.ptr(ws, torch.uint8, "ws"),
-                                        ws.numel(), _stream()), "replay_kv_attention")
+    B, H, Hkv, D, dev = end.shape[0], layer.nheads, layer.nkv, layer.head_dim, _on_device(K.device)
+    shape = (layer.npages, Hkv, layer.page_size, D)
+    if table.dim() != 2:
+        raise ValueError("table must be [B][max_pages]")
+    mp = table.shape[1]
+    if o is None:
+        o = torch.zeros((ntok, B, H, D), dtype=io, device=dev)
+    a = KVAttentionArgs(K=_addr(K, dev, kind, "K", shape), V=_addr(V, dev, kind, "V", shape),
+                        table=_addr(table, dev, torch.int32, "table", (B, mp)), end=_addr(end, dev, torch.int32, "end", (B,)),
+                        batch=B, max_pages=mp, ntok=ntok, window=window, scale=D ** -0.5 if scale is None else scale,
+                        o=_addr(o, dev, io, "o", (ntok, B, H, D)))
+    a.q, a.q_stride = _rows(q, dev, io, "q", ntok * B, H * D)
+    if k_scale is not None or v_scale is not None:
+        a.k_scale = _addr(k_scale, dev, torch.float32, "k_scale", (Hkv,))
+        a.v_scale = _addr(v_scale, dev, torch.float32, "v_scale", (Hkv,))
+    if active is not None:
+        a.active = _addr(active, dev, torch.uint8, "active", (B,))
+    if lse is not None:
+        a.lse = _addr(lse, dev, torch.float32, "lse", (ntok, B, H))
+    if err is not None:
+        a.err = _addr(err, dev, torch.int32, "err", (1,))
+    if ws is None:
+        ws = torch.empty(max(1, kv_attention_workspace(layer, B, ntok)), dtype=torch.uint8, device=dev)
+    _launch(dev, "replay_kv_attention", _lib.replay_kv_attention, ctypes.byref(layer), ctypes.byref(a),
+            _addr(ws, dev, torch.uint8, "ws"), ws.numel())
     return o
 
 
