@@ -3,40 +3,89 @@
 //
 // A row is (Hq + 2 Hkv) heads of D channels.  Its work items are pairs of 16-byte chunks: in the
 // halves style a chunk of eight channels and the chunk rot_dim / 2 further, so that both ends of
-// eight rotated pairs are in one lane; elsewhere two neighbouring chunks.  The row's cosines and
-// sines are formed once, in LDS, and serve all of its heads: the angle is pos * freq in fp64 as a
-// fraction of a turn (exact to 2^-52 of the number of turns, so a position of 10^6 still has its
-// angle to 10^-9), the fraction goes to sincospi in fp32.
+// eight rotated pairs are in one lane; elsewhere two chunks half a run apart, so that neighbouring
+// lanes write neighbouring chunks (32-byte pieces per lane cost streamed stores 40 %).  The row's
+// cosines and sines are formed once, in LDS, and serve all of its heads: the angle is pos * freq in
+// fp64 as a fraction of a turn (exact to 2^-52 of the number of turns, so a position of 10^6 still has
+// its angle to 10^-9), the fraction goes to sincospi in fp32.
 //
-// Bound by HBM: q, k and v are read once and written once.
+// Bound by HBM: q, k and v are read once and written once.  16387 rows of 32 + 2 x 8 heads of 128
+// channels, 403 MB: 73 us, 5.5 TB/s, against 5.9 TB/s of a copy.
 #include <type_traits>
 
 #include "kv_io.hpp"
 
 namespace rs {
 
+// Stores of large calls bypass the caches: nothing reads those rows again soon.
+template <bool STREAM, typename T>
+__device__ __forceinline__ void kv_store(T* p, T v)
+{
+    if constexpr (STREAM) __builtin_nontemporal_store(v, p);
+    else *p = v;
+}
+
 // One 16-byte chunk in registers to the cache, as io elements or as E4M3 codes of x / scale.
-template <int IO, bool FP8>
+template <int IO, bool FP8, bool STREAM>
 __device__ __forceinline__ void store_cached(void* cache, size_t at, const float (&x)[8], float scale)
 {
     if constexpr (FP8) {
         // a true division: the code is that of the correctly rounded quotient
         const u32x2 w = {pack_e4m3(f32x4{x[0] / scale, x[1] / scale, x[2] / scale, x[3] / scale}),
                          pack_e4m3(f32x4{x[4] / scale, x[5] / scale, x[6] / scale, x[7] / scale})};
-        *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(cache) + at) = w;
+        kv_store<STREAM>(reinterpret_cast<u32x2*>(static_cast<uint8_t*>(cache) + at), w);
     } else {
-        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(cache) + at) = kv_pack8<IO>(x);
+        kv_store<STREAM>(reinterpret_cast<u32x4*>(static_cast<uint16_t*>(cache) + at), kv_pack8<IO>(x));
     }
 }
 
-// R rows per workgroup.
-template <int IO, bool FP8, int STYLE, int R>
+// R rows per workgroup, U items of a thread in flight at a time.  The first items are requested before
+// the angles are formed.
+template <int IO, bool FP8, int STYLE, int R, int U>
 __global__ __launch_bounds__(256) void kv_append_kernel(KvAppend a, int log_items)
 {
     __shared__ float2 turn[R][128];      // cos, sin of each rotated pair
     __shared__ int64_t slot[R];
     const int tid = threadIdx.x, row0 = blockIdx.x * R;
-    const int pairs = a.rot >> 1;
+    const int pairs = a.rot >> 1, rot_items = a.rot >> 4;    // items of a head with rotated channels
+    const int h0 = a.q ? 0 : a.Hq, heads = a.Hq - h0 + 2 * a.Hkv;
+    const int per_row = heads << log_items;                  // D / 16 items per head
+    const int total = min(R, a.rows - row0) * per_row;
+    u32x4 w[U][2];
+    // row, head and item of index i, and its two chunks' first channels
+    struct Item {
+        int r, h, it, c0, c1;
+    };
+    auto item = [&](int i) {
+        Item x;
+        x.r = 0;
+#pragma unroll
+        for (int k = 1; k < R; ++k) x.r += i >= k * per_row ? 1 : 0;
+        const int j = i - x.r * per_row;
+        x.h = h0 + (j >> log_items);
+        x.it = j & ((1 << log_items) - 1);
+        // neighbouring items are neighbouring chunks: halves of the rotated channels and of the rest, or
+        // of the whole head where pairs are neighbours
+        const bool rest = STYLE == KV_ROT_HALVES && x.it >= rot_items;
+        x.c0 = 8 * (rest ? x.it + rot_items : x.it);
+        x.c1 = x.c0 + (STYLE == KV_ROT_HALVES ? (rest ? (a.D - a.rot) >> 1 : pairs) : a.D >> 1);
+        return x;
+    };
+    auto request = [&](int base) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = base + u * 256;
+            if (i >= total) continue;
+            const Item x = item(i);
+            const size_t row = (size_t)(row0 + x.r);
+            const uint16_t* src;
+            if (x.h < a.Hq) src = static_cast<const uint16_t*>(a.q) + row * a.q_stride + (size_t)x.h * a.D;
+            else if (x.h < a.Hq + a.Hkv) src = static_cast<const uint16_t*>(a.k) + row * a.k_stride + (size_t)(x.h - a.Hq) * a.D;
+            else src = static_cast<const uint16_t*>(a.v) + row * a.v_stride + (size_t)(x.h - a.Hq - a.Hkv) * a.D;
+            w[u][0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(src + x.c0));
+            w[u][1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(src + x.c1));
+        }
+    };
     if (tid < R) {
         int64_t s = row0 + tid < a.rows ? a.slots[row0 + tid] : -1;
         if (s >= a.nslots) {
@@ -45,6 +94,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppend a, int log_item
         }
         slot[tid] = s;
     }
+    request(tid);
     for (int i = tid; i < R * pairs; i += 256) {
         const int r = i / pairs, p = i - r * pairs;
         if (row0 + r < a.rows) {
@@ -60,64 +110,58 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppend a, int log_item
         }
     }
     __syncthreads();
-    const int heads = (a.q ? a.Hq : 0) + 2 * a.Hkv;
-    const int per_row = heads << log_items;                  // D / 16 items per head
-    const int rot_items = a.rot >> 4;                        // items of a head with rotated channels
-    const int h0 = a.q ? 0 : a.Hq;
 #pragma unroll 1
-    for (int i = tid; i < R * per_row; i += 256) {
-        const int r = R == 1 ? 0 : i / per_row;
-        const int64_t sl = slot[r];
-        if (sl < 0) continue;
-        const int j = i - r * per_row;
-        const int h = h0 + (j >> log_items), it = j & ((1 << log_items) - 1);
-        const size_t row = (size_t)(row0 + r);
-        const uint16_t* src;
-        int hk = 0;
-        if (h < a.Hq) src = static_cast<const uint16_t*>(a.q) + row * a.q_stride + (size_t)h * a.D;
-        else if (h < a.Hq + a.Hkv) src = static_cast<const uint16_t*>(a.k) + row * a.k_stride + (size_t)(hk = h - a.Hq) * a.D;
-        else src = static_cast<const uint16_t*>(a.v) + row * a.v_stride + (size_t)(hk = h - a.Hq - a.Hkv) * a.D;
-        const bool turned = it < rot_items && h < a.Hq + a.Hkv;
-        // the item's two chunks (first channel of each)
-        const bool apart = STYLE == KV_ROT_HALVES && it < rot_items;
-        const int c0 = apart ? 8 * it : 16 * it, c1 = apart ? c0 + pairs : c0 + 8;
-        float x[8], y[8];
-        kv_unpack8<IO>(__builtin_nontemporal_load(reinterpret_cast<const u32x4*>(src + c0)), x);
-        kv_unpack8<IO>(__builtin_nontemporal_load(reinterpret_cast<const u32x4*>(src + c1)), y);
-        if (turned) {
-            if constexpr (STYLE == KV_ROT_HALVES) {
+    for (int base = tid; base < total; base += 256 * U) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float2 cs = turn[r][c0 + e];
-                    const float u = x[e], w = y[e];
-                    x[e] = u * cs.x - w * cs.y;
-                    y[e] = w * cs.x + u * cs.y;
+        for (int u = 0; u < U; ++u) {
+            if (base + u * 256 >= total) continue;
+            const Item t = item(base + u * 256);
+            const int64_t sl = slot[t.r];
+            if (sl < 0) continue;
+            const bool is_q = t.h < a.Hq, is_k = !is_q && t.h < a.Hq + a.Hkv;
+            float x[8], y[8];
+            kv_unpack8<IO>(w[u][0], x);
+            kv_unpack8<IO>(w[u][1], y);
+            if (is_q || is_k) {
+                if (STYLE == KV_ROT_HALVES && t.it < rot_items) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float2 cs = turn[t.r][t.c0 + e];
+                        const float p = x[e], q = y[e];
+                        x[e] = p * cs.x - q * cs.y;
+                        y[e] = q * cs.x + p * cs.y;
+                    }
                 }
-            } else {
+                if constexpr (STYLE == KV_ROT_ADJACENT) {
+                    auto turn_chunk = [&](float (&z)[8], int c) {
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    const float2 c = turn[r][(c0 + e) >> 1], d = turn[r][(c1 + e) >> 1];
-                    const float u = x[e], w = x[e + 1], s = y[e], t = y[e + 1];
-                    x[e] = u * c.x - w * c.y;
-                    x[e + 1] = w * c.x + u * c.y;
-                    y[e] = s * d.x - t * d.y;
-                    y[e + 1] = t * d.x + s * d.y;
+                        for (int e = 0; e < 8; e += 2) {
+                            const float2 cs = turn[t.r][(c + e) >> 1];
+                            const float p = z[e], q = z[e + 1];
+                            z[e] = p * cs.x - q * cs.y;
+                            z[e + 1] = q * cs.x + p * cs.y;
+                        }
+                    };
+                    if (t.c0 < a.rot) turn_chunk(x, t.c0);
+                    if (t.c1 < a.rot) turn_chunk(y, t.c1);
                 }
             }
+            constexpr bool STREAM = R > 1;
+            if (is_q) {
+                uint16_t* dst = static_cast<uint16_t*>(a.q_out) + ((size_t)(row0 + t.r) * a.Hq + t.h) * a.D;
+                kv_store<STREAM>(reinterpret_cast<u32x4*>(dst + t.c0), kv_pack8<IO>(x));
+                kv_store<STREAM>(reinterpret_cast<u32x4*>(dst + t.c1), kv_pack8<IO>(y));
+            } else {
+                const int hk = t.h - a.Hq - (is_k ? 0 : a.Hkv);
+                void* cache = is_k ? a.K : a.V;
+                const size_t page = (size_t)(sl >> a.page_shift), off = (size_t)sl & ((1u << a.page_shift) - 1);
+                const size_t at = (((page * a.Hkv + hk) << a.page_shift) + off) * a.D;
+                const float scale = FP8 ? (is_k ? a.k_scale : a.v_scale)[hk] : 1.f;
+                store_cached<IO, FP8, STREAM>(cache, at + t.c0, x, scale);
+                store_cached<IO, FP8, STREAM>(cache, at + t.c1, y, scale);
+            }
         }
-        if (h < a.Hq) {
-            uint16_t* dst = static_cast<uint16_t*>(a.q_out) + (row * a.Hq + h) * a.D;
-            *reinterpret_cast<u32x4*>(dst + c0) = kv_pack8<IO>(x);
-            *reinterpret_cast<u32x4*>(dst + c1) = kv_pack8<IO>(y);
-        } else {
-            const bool is_k = h < a.Hq + a.Hkv;
-            void* cache = is_k ? a.K : a.V;
-            const size_t page = (size_t)(sl >> a.page_shift), off = (size_t)sl & ((1u << a.page_shift) - 1);
-            const size_t at = (((page * a.Hkv + hk) << a.page_shift) + off) * a.D;
-            const float scale = FP8 ? (is_k ? a.k_scale : a.v_scale)[hk] : 1.f;
-            store_cached<IO, FP8>(cache, at + c0, x, scale);
-            store_cached<IO, FP8>(cache, at + c1, y, scale);
-        }
+        if (base + 256 * U < total) request(base + 256 * U);
     }
 }
 
@@ -125,10 +169,13 @@ template <int IO, bool FP8, int STYLE>
 static void start(const KvAppend& a, hipStream_t s)
 {
     const int log_items = a.D == 64 ? 2 : (a.D == 128 ? 3 : 4);
+    // Up to some rows a CU the latency of one counts, and what they write is read by the attention that
+    // follows; past that two rows share a workgroup (2048 rows 11.4 us with four, 9.4 with two), and
+    // streamed stores pay (16387 rows 80 -> 73 us).
     if (a.rows <= 1024) {
-        hipLaunchKernelGGL((kv_append_kernel<IO, FP8, STYLE, 1>), dim3(a.rows), dim3(256), 0, s, a, log_items);
+        hipLaunchKernelGGL((kv_append_kernel<IO, FP8, STYLE, 1, 2>), dim3(a.rows), dim3(256), 0, s, a, log_items);
     } else {
-        hipLaunchKernelGGL((kv_append_kernel<IO, FP8, STYLE, 4>), dim3((a.rows + 3) / 4), dim3(256), 0, s, a, log_items);
+        hipLaunchKernelGGL((kv_append_kernel<IO, FP8, STYLE, 2, 3>), dim3((a.rows + 1) / 2), dim3(256), 0, s, a, log_items);
     }
 }
 
