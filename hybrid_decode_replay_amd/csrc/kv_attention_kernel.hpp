@@ -357,32 +357,46 @@ struct KvRows {
     }
 
     // Raw scores of 32 tokens; kf(blk, piece) gives 16 bytes of K, q the queries in LDS.
-    // FENCE: operands of at most that many products along the head are read ahead (registers).
-    template <int FENCE, typename KF>
+    // FROM_LDS: K is there too; two products' operands are read while the two before them run, and no
+    // more than that ahead (registers).
+    template <bool FROM_LDS, typename KF>
     __device__ __forceinline__ void scores(f32x4 (&s)[RB][2], const u32x4 (*q)[64], int lane, KF kf) const
     {
+        constexpr int P = FP8 ? 1 : 2;                       // pieces of K that two products take
+        u32x4 kw[2][2][P], qw[2][2][RB];
+        auto read = [&](int i) {
+#pragma unroll
+            for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+                for (int x = 0; x < P; ++x) kw[i & 1][blk][x] = kf(blk, i * P + x);
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb) qw[i & 1][x][rb] = q[rb * KS + 2 * i + x][lane];
+        };
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb) s[rb][0] = s[rb][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+        read(0);
 #pragma unroll
-        for (int i = 0; i < KS; ++i) {
-            u32x4 qf[RB];
+        for (int i = 0; i < KS / 2; ++i) {
+            if (i + 1 < KS / 2) read(i + 1);
+            if constexpr (FROM_LDS) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int rb = 0; rb < RB; ++rb) qf[rb] = q[rb * KS + i][lane];
+            for (int x = 0; x < 2; ++x)
 #pragma unroll
-            for (int blk = 0; blk < 2; ++blk) {
-                u32x4 A;
-                if constexpr (FP8) {
-                    const u32x4 w = kf(blk, i >> 1);
-                    const uint32_t w0 = (i & 1) ? w.z : w.x, w1 = (i & 1) ? w.w : w.y;
-                    A = u32x4{kv_from_e4m3<IO, false>(w0), kv_from_e4m3<IO, true>(w0),
-                              kv_from_e4m3<IO, false>(w1), kv_from_e4m3<IO, true>(w1)};
-                } else {
-                    A = kf(blk, i);
+                for (int blk = 0; blk < 2; ++blk) {
+                    u32x4 A;
+                    if constexpr (FP8) {
+                        const u32x4 w = kw[i & 1][blk][0];
+                        const uint32_t w0 = x ? w.z : w.x, w1 = x ? w.w : w.y;
+                        A = u32x4{kv_from_e4m3<IO, false>(w0), kv_from_e4m3<IO, true>(w0),
+                                  kv_from_e4m3<IO, false>(w1), kv_from_e4m3<IO, true>(w1)};
+                    } else {
+                        A = kw[i & 1][blk][x];
+                    }
+#pragma unroll
+                    for (int rb = 0; rb < RB; ++rb) s[rb][blk] = kv_mfma<IO>(A, qw[i & 1][x][rb], s[rb][blk]);
                 }
-#pragma unroll
-                for (int rb = 0; rb < RB; ++rb) s[rb][blk] = kv_mfma<IO>(A, qf[rb], s[rb][blk]);
-            }
-            if (FENCE > 0 && (i + 1) % (FENCE > 0 ? FENCE : 1) == 0) __builtin_amdgcn_sched_barrier(0);
         }
     }
 
@@ -508,8 +522,8 @@ struct KvRows {
     {
         u32x4 ph[RB], pl[RB];
         const bool mine[RB] = {};
+        values();                            // (on their way while the weights are formed)
         weights(s, p.sc_abs(), ph, pl);
-        values();
         outputs<false>(ph, pl, mine);
     }
 
@@ -726,7 +740,7 @@ __global__ __launch_bounds__(256, OCC) void kv_attention_kernel(KvAttention a)
         };
         auto scores = [&](f32x4 (&s)[RB][2]) {
             asm volatile("" ::: "memory");           // queries stay in LDS from block to block
-            rows.template scores<0>(s, sh.q[wv], lane, [&](int blk, int i) { return kf[blk][i]; });
+            rows.template scores<false>(s, sh.q[wv], lane, [&](int blk, int i) { return kf[blk][i]; });
         };
         auto masked = [&](auto more) {
             f32x4 s[RB][2];
@@ -850,7 +864,7 @@ __global__ __launch_bounds__(512, 1) void kv_attention_wide_kernel(KvAttention a
         const int fold = (n / FT) & FM;
         auto scores = [&](f32x4 (&s)[RB][2], int sb) {
             const uint8_t* ks = sh.kv[0] + (sb * KV_SUB + n) * ROWB;
-            rows.template scores<2>(s, s_q[rg], lane, [&](int blk, int i) {
+            rows.template scores<true>(s, s_q[rg], lane, [&](int blk, int i) {
                 return *reinterpret_cast<const u32x4*>(ks + blk * 16 * ROWB + ((i * 4 + g) ^ fold) * 16);
             });
             __builtin_amdgcn_sched_barrier(0);                   // V is read when K is used up
