@@ -28,7 +28,7 @@ KvPlan kv_attention_plan(int D, bool fp8, int rows)
     const int most = 16 * p.RB * p.RW;
     p.rpc = rows < most ? rows : most;
     p.nchunk = (rows + most - 1) / most;
-    p.nwg = 256 * (p.wide ? 1 : kv_occ(D, fp8, p.RB));
+    p.nwg = 256 * (p.wide ? 2 : kv_occ(D, fp8, p.RB));
     return p;
 }
 

@@ -783,41 +783,47 @@ __global__ __launch_bounds__(256, OCC) void kv_attention_kernel(KvAttention a)
     }
 }
 
-// More rows: eight waves in RW row groups of 16 RB rows, the 8 / RW waves of a group splitting its
+// More rows: four waves in RW row groups of 16 RB rows, the 4 / RW waves of a group splitting its
 // tokens.  The cache passes through LDS in stages of ST tokens, so that it is read once for all
 // rows: each wave requests its eighth of the next stage into registers, and writes it to LDS when
 // the workgroup is through with the stage before.  K's 16-byte pieces are permuted within a token
 // (fold) so that 16 tokens' equal pieces lie in different banks.
 template <int IO, bool FP8, int D, int RB, int RW>
-__global__ __launch_bounds__(512, 1) void kv_attention_wide_kernel(KvAttention a)
+__global__ __launch_bounds__(256, 2) void kv_attention_wide_kernel(KvAttention a)
 {
     using G = KvGeom<FP8, D>;
     using R = KvRows<IO, FP8, D, RB>;
-    constexpr int NTW = 8 / RW, EB = G::EB, VE = G::VE, VL = G::VL, VW = G::VW, ROWB = G::ROWB;
-    constexpr int ST = ROWB <= 256 ? KV_TILE : KV_TILE / 2;      // tokens of a stage
+    constexpr int NTW = 4 / RW, EB = G::EB, VE = G::VE, VL = G::VL, VW = G::VW, ROWB = G::ROWB;
+    constexpr int ST = ROWB <= 128 ? KV_TILE : 16384 / ROWB;     // tokens of a stage
     constexpr int CPB = 16 * ROWB / 1024;                        // 1 KiB chunks of 16 tokens
     constexpr int NC = ST / 16 * CPB;                            // chunks of K, and of V
-    constexpr int CJ = NC / 8;                                   // of them a wave's
+    constexpr int CJ = NC / 4;                                   // of them a wave's
     constexpr int TPC = 1024 / ROWB;                             // tokens of a chunk
     constexpr int FT = ROWB >= 256 ? 1 : 256 / ROWB, FM = ROWB / 16 < 16 ? ROWB / 16 - 1 : 15;
     constexpr int JP = 4;
-    static_assert(NC % 8 == 0 && 8 % CPB == 0, "every wave takes whole chunks");
+    constexpr int CV = CPB > 4 ? CPB / 4 : 1;                    // different parts of a block a wave takes
+    static_assert(NC % 4 == 0 && CJ % CV == 0 && (CPB > 4 || 4 % CPB == 0), "every wave takes whole chunks");
     extern __shared__ int s_pre[];
     __shared__ union alignas(16) {
         uint8_t kv[2][ST * ROWB];                                // a stage of K and of V
-        float o[8][16][16 * JP + 4];
+        float o[4][16][16 * JP + 4];
     } sh;
     __shared__ u32x4 s_q[RW][RB * G::KS][64];
-    __shared__ float s_m[8][16], s_l[8][16];
-    __shared__ int s_wave[8];
+    __shared__ float s_m[4][16], s_l[4][16];
+    __shared__ int s_wave[4];
     const int lane = threadIdx.x & 63, wv = uni(threadIdx.x >> 6), rg = wv % RW, tw = wv / RW, n = lane & 15, g = lane >> 4;
     KvLine ln;
     KvPart p;
-    if (a.whole ? !kv_whole_part<FP8>(a, p) : !kv_line<512>(a, s_pre, s_wave, ln)) return;
-    // a wave's chunks are the same part of blocks wv / CPB, wv / CPB + 8 / CPB, ..; the lane's bytes there
-    const int part = wv % CPB, blk0 = wv / CPB, tok = part * TPC + lane * 16 / ROWB, pos = lane * 16 % ROWB / 16;
-    const uint32_t voff = part * 1024 + lane * 16;
-    const uint32_t koff = tok * ROWB + (pos ^ ((tok / FT) & FM)) * 16;
+    if (a.whole ? !kv_whole_part<FP8>(a, p) : !kv_line<256>(a, s_pre, s_wave, ln)) return;
+    // chunk j of a wave is chunk wv + 4 j of the stage: block, and the lane's bytes in the block
+    auto block_of = [&](int j) { return (wv + 4 * j) / CPB; };
+    uint32_t koff[CV], voff[CV];
+#pragma unroll
+    for (int c = 0; c < CV; ++c) {
+        const int part = (wv + 4 * c) % CPB, tok = part * TPC + lane * 16 / ROWB, pos = lane * 16 % ROWB / 16;
+        voff[c] = part * 1024 + lane * 16;
+        koff[c] = tok * ROWB + (pos ^ ((tok / FT) & FM)) * 16;
+    }
 #pragma unroll 1
     while (a.whole || ln.u < ln.u1) {
         if (!a.whole) p = kv_line_part<FP8>(a, s_pre, ln);
@@ -830,14 +836,14 @@ __global__ __launch_bounds__(512, 1) void kv_attention_wide_kernel(KvAttention a
         uint32_t entry[CJ];                                      // and the pages of those after it
         auto pages = [&](int st) {
 #pragma unroll
-            for (int j = 0; j < CJ; ++j) entry[j] = kv_page_of(a, p, st + 16 * (blk0 + j * (8 / CPB)));
+            for (int j = 0; j < CJ; ++j) entry[j] = kv_page_of(a, p, st + 16 * block_of(j));
         };
         auto request = [&](int st) {
 #pragma unroll
             for (int j = 0; j < CJ; ++j) {
-                const size_t at = kv_locate<ROWB>(a, p, entry[j], st + 16 * (blk0 + j * (8 / CPB)));
-                kr[j] = kv_stream<u32x4>(Kc + at + koff);
-                vr[j] = kv_stream<u32x4>(Vc + at + voff);
+                const size_t at = kv_locate<ROWB>(a, p, entry[j], st + 16 * block_of(j));
+                kr[j] = kv_stream<u32x4>(Kc + at + koff[j % CV]);
+                vr[j] = kv_stream<u32x4>(Vc + at + voff[j % CV]);
             }
             pages(st + ST);
         };
@@ -854,7 +860,7 @@ __global__ __launch_bounds__(512, 1) void kv_attention_wide_kernel(KvAttention a
             __syncthreads();                                     // the stage before is used up
 #pragma unroll
             for (int j = 0; j < CJ; ++j) {
-                const int c = wv + 8 * j;
+                const int c = wv + 4 * j;
                 *reinterpret_cast<u32x4*>(sh.kv[0] + c * 1024 + lane * 16) = kr[j];
                 *reinterpret_cast<u32x4*>(sh.kv[1] + c * 1024 + lane * 16) = vr[j];
             }
@@ -907,7 +913,7 @@ __global__ __launch_bounds__(512, 1) void kv_attention_wide_kernel(KvAttention a
                 st += ST;
             }
         }
-        rows.template join<512, RW, NTW, JP>(a, p, sh.o, s_m, s_l);
+        rows.template join<256, RW, NTW, JP>(a, p, sh.o, s_m, s_l);
         if (a.whole) break;
         kv_next(a, p, s_pre, ln);
     }
@@ -998,10 +1004,10 @@ static hipError_t kv_attention_width(const KvAttention& a, const KvPlan& p, hipS
     const dim3 grid(a.whole ? ranges : p.nwg);
     if (p.wide) {
         if constexpr (D == 256) {
-            hipLaunchKernelGGL((kv_attention_wide_kernel<IO, FP8, D, 1, 4>), grid, dim3(512), lds, s, a);
+            hipLaunchKernelGGL((kv_attention_wide_kernel<IO, FP8, D, 1, 4>), grid, dim3(256), lds, s, a);
         } else {
-            if (p.RW == 2) hipLaunchKernelGGL((kv_attention_wide_kernel<IO, FP8, D, 2, 2>), grid, dim3(512), lds, s, a);
-            else hipLaunchKernelGGL((kv_attention_wide_kernel<IO, FP8, D, 2, 4>), grid, dim3(512), lds, s, a);
+            if (p.RW == 2) hipLaunchKernelGGL((kv_attention_wide_kernel<IO, FP8, D, 2, 2>), grid, dim3(256), lds, s, a);
+            else hipLaunchKernelGGL((kv_attention_wide_kernel<IO, FP8, D, 2, 4>), grid, dim3(256), lds, s, a);
         }
     } else if (p.RB == 2) {
         hipLaunchKernelGGL((kv_attention_kernel<IO, FP8, D, 2, kv_occ(D, FP8, 2)>), grid, dim3(256), lds, s, a);
