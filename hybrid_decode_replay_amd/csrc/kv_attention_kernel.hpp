@@ -310,8 +310,9 @@ __device__ __forceinline__ size_t kv_locate(const KvAttention& a, const KvPart& 
     return wave_uniform(((size_t)page * a.Hkv + p.hkv) * head + (size_t)off * ROWB);
 }
 
-// The rows of one wave: RB blocks of 16, their softmax state and outputs, and 32 tokens' values.
-template <int IO, bool FP8, int D, int RB>
+// The rows of one wave: RB blocks of 16, their softmax state and outputs, and 32 tokens' values, of
+// which VP pieces (of VL) are held at a time.
+template <int IO, bool FP8, int D, int RB, int VP>
 struct KvRows {
     using G = KvGeom<FP8, D>;
     static constexpr int KS = G::KS, JN = G::JN, VE = G::VE, VL = G::VL, VW = G::VW;
@@ -320,7 +321,7 @@ struct KvRows {
     float m[RB], l[RB];
     f32x4 O[RB][JN];
     int lim_hi[RB], lim_lo[RB];              // visible positions of the lane's row
-    uint32_t vf[2][4][VL][VW];               // values of tokens 16 blk + 4 (lane / 16) + r
+    uint32_t vf[2][4][VP][VW];               // values of tokens 16 blk + 4 (lane / 16) + r
 
     __device__ __forceinline__ void init()
     {
@@ -439,9 +440,9 @@ struct KvRows {
         }
     }
 
-    // O += V^T P^T for the 32 tokens in vf, of all rows or of those in mine.
+    // O += V^T P^T for the pieces v0.. of the 32 tokens in vf, of all rows or of those in mine.
     template <bool SOME>
-    __device__ __forceinline__ void outputs(const u32x4 (&ph)[RB], const u32x4 (&pl)[RB], const bool (&mine)[RB])
+    __device__ __forceinline__ void outputs(int v0, const u32x4 (&ph)[RB], const u32x4 (&pl)[RB], const bool (&mine)[RB])
     {
         auto add = [&](u32x4 A, int j) {
 #pragma unroll
@@ -453,7 +454,7 @@ struct KvRows {
             if constexpr (SOME) __builtin_amdgcn_sched_barrier(0);
         };
 #pragma unroll
-        for (int v = 0; v < VL; ++v) {
+        for (int v = 0; v < VP; ++v) {
             if constexpr (FP8) {
 #pragma unroll
                 for (int w = 0; w < VW; ++w) {
@@ -470,7 +471,7 @@ struct KvRows {
                         e[3][t] = kv_from_e4m3<IO, true>(c23);
                     }
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) add(u32x4{e[c][0], e[c][1], e[c][2], e[c][3]}, v * VE + w * 4 + c);
+                    for (int c = 0; c < 4; ++c) add(u32x4{e[c][0], e[c][1], e[c][2], e[c][3]}, (v0 + v) * VE + w * 4 + c);
                 }
             } else {
 #pragma unroll
@@ -480,7 +481,7 @@ struct KvRows {
                     add(u32x4{__builtin_amdgcn_perm(vf[0][1][v][w], vf[0][0][v][w], sel),
                               __builtin_amdgcn_perm(vf[0][3][v][w], vf[0][2][v][w], sel),
                               __builtin_amdgcn_perm(vf[1][1][v][w], vf[1][0][v][w], sel),
-                              __builtin_amdgcn_perm(vf[1][3][v][w], vf[1][2][v][w], sel)}, v * VE + c);
+                              __builtin_amdgcn_perm(vf[1][3][v][w], vf[1][2][v][w], sel)}, (v0 + v) * VE + c);
                 }
             }
         }
@@ -494,7 +495,7 @@ struct KvRows {
             const int t = mt + (e >> 2) * 16 + (e & 3);
             const bool sees = t < hi && t >= lo && (e < 4 ? ok0 : ok1);
 #pragma unroll
-            for (int v = 0; v < VL; ++v)
+            for (int v = 0; v < VP; ++v)
 #pragma unroll
                 for (int w = 0; w < VW; ++w) vf[e >> 2][e & 3][v][w] = sees ? vf[e >> 2][e & 3][v][w] : 0u;
         }
@@ -508,7 +509,7 @@ struct KvRows {
             const int t = mt + (e >> 2) * 16 + (e & 3);
             uint32_t y = 0;
 #pragma unroll
-            for (int v = 0; v < VL; ++v)
+            for (int v = 0; v < VP; ++v)
 #pragma unroll
                 for (int w = 0; w < VW; ++w) y |= kv_odd<IO, FP8>(vf[e >> 2][e & 3][v][w]);
             x |= t < p.all_lo || t >= p.all_hi ? y : 0u;
@@ -516,19 +517,24 @@ struct KvRows {
         return __builtin_amdgcn_ballot_w64(x != 0) != 0;
     }
 
-    // 32 tokens that every row sees, whose raw scores are s: weights and outputs.  values() fills vf.
+    // 32 tokens that every row sees, whose raw scores are s: weights and outputs.  values(v0) fills vf
+    // with pieces v0...
     template <typename VF>
     __device__ __forceinline__ void take(const KvPart& p, const f32x4 (&s)[RB][2], VF values)
     {
         u32x4 ph[RB], pl[RB];
         const bool mine[RB] = {};
-        values();                            // (on their way while the weights are formed)
+        values(0);                           // (on their way while the weights are formed)
         weights(s, p.sc_abs(), ph, pl);
-        outputs<false>(ph, pl, mine);
+#pragma unroll
+        for (int v = 0; v < VL; v += VP) {
+            if (v > 0) values(v);
+            outputs<false>(v, ph, pl, mine);
+        }
     }
 
     // The 32 tokens at t0, whoever sees them.  ok0, ok1: the two blocks' pages are in the cache.
-    // values(again) fills vf.
+    // values(v0, again) fills vf; again: not for the first time.
     template <typename VF>
     __device__ __forceinline__ void take_masked(const KvAttention& a, const KvPart& p, f32x4 (&s)[RB][2], int t0, bool ok0,
                                                 bool ok1, int lane, VF values)
@@ -547,20 +553,34 @@ struct KvRows {
         // Values that no row sees count as zero, so that 0 * NaN does not arise.  A value that only some
         // drafts see and that is no number would still reach the others: then, and only then, the drafts
         // are taken one by one.
+        const int lo = a.window > 0 ? max(0, p.all_hi - a.window) : 0;           // of any row
         bool apart = false;
-#pragma unroll 1
-        for (int d = -1; d < (apart ? a.T : 0); ++d) {
-            const int hi = d < 0 ? p.end : p.all_hi + d;
-            values(d >= 0);
-            clear(mt, a.window > 0 ? max(0, (d < 0 ? p.all_hi : hi) - a.window) : 0, hi, ok0, ok1);
-            if (d < 0 && a.T > 1 && odd(p, mt)) {
-                apart = true;
-                continue;
+        if constexpr (VP < VL) {                         // the pieces are not held: looked through first
+            if (a.T > 1) {
+#pragma unroll
+                for (int v = 0; v < VL; v += VP) {
+                    values(v, false);
+                    clear(mt, lo, p.end, ok0, ok1);
+                    apart |= odd(p, mt);
+                }
             }
+        }
+#pragma unroll 1
+        for (int d = apart ? 0 : -1; d < (apart ? a.T : 0); ++d) {
+            const int hi = d < 0 ? p.end : p.all_hi + d;
             bool mine[RB];
 #pragma unroll
             for (int rb = 0; rb < RB; ++rb) mine[rb] = d < 0 || lim_hi[rb] == hi;
-            outputs<true>(ph, pl, mine);
+#pragma unroll
+            for (int v = 0; v < VL; v += VP) {
+                values(v, d >= 0);
+                clear(mt, d < 0 ? lo : (a.window > 0 ? max(0, hi - a.window) : 0), hi, ok0, ok1);
+                if (VP == VL && d < 0 && a.T > 1 && odd(p, mt)) {
+                    apart = true;
+                    continue;
+                }
+                outputs<true>(v, ph, pl, mine);
+            }
         }
     }
 
@@ -658,7 +678,7 @@ template <int IO, bool FP8, int D, int RB, int OCC>
 __global__ __launch_bounds__(256, OCC) void kv_attention_kernel(KvAttention a)
 {
     using G = KvGeom<FP8, D>;
-    using R = KvRows<IO, FP8, D, RB>;
+    using R = KvRows<IO, FP8, D, RB, G::VL>;
     constexpr int JP = G::JN < 8 ? G::JN : 8, EB = G::EB, VE = G::VE, VL = G::VL, VW = G::VW, KL = G::KL;
     extern __shared__ int s_pre[];
     // the waves' queries while tokens pass, their outputs when they are joined
@@ -749,7 +769,7 @@ __global__ __launch_bounds__(256, OCC) void kv_attention_kernel(KvAttention a)
             const size_t cb0 = b0, cb1 = b1;
             const bool ok0 = c0 < (uint32_t)a.npages, ok1 = c1 < (uint32_t)a.npages;
             if constexpr (decltype(more)::value) next_k();
-            rows.take_masked(a, p, s, cur, ok0, ok1, lane, [&](bool again) {
+            rows.take_masked(a, p, s, cur, ok0, ok1, lane, [&](int, bool again) {
                 if (again) load_v(cb0, cb1);
             });
             if constexpr (decltype(more)::value) next_v();
@@ -762,7 +782,7 @@ __global__ __launch_bounds__(256, OCC) void kv_attention_kernel(KvAttention a)
                 f32x4 s[RB][2];
                 scores(s);
                 next_k();
-                rows.take(p, s, [] {});
+                rows.take(p, s, [](int) {});
                 next_v();
             }
         }
@@ -772,7 +792,7 @@ __global__ __launch_bounds__(256, OCC) void kv_attention_kernel(KvAttention a)
                 if ((taken = !wrong && p.full(t0, KV_SUB))) {
                     f32x4 s[RB][2];
                     scores(s);
-                    rows.take(p, s, [] {});
+                    rows.take(p, s, [](int) {});
                 }
             }
             if (!taken) masked(std::false_type{});
@@ -792,8 +812,8 @@ template <int IO, bool FP8, int D, int RB, int RW>
 __global__ __launch_bounds__(256, 2) void kv_attention_wide_kernel(KvAttention a)
 {
     using G = KvGeom<FP8, D>;
-    using R = KvRows<IO, FP8, D, RB>;
-    constexpr int NTW = 4 / RW, EB = G::EB, VE = G::VE, VL = G::VL, VW = G::VW, ROWB = G::ROWB;
+    using R = KvRows<IO, FP8, D, RB, 1>;
+    constexpr int NTW = 4 / RW, EB = G::EB, VE = G::VE, VW = G::VW, ROWB = G::ROWB;
     constexpr int ST = ROWB <= 128 ? KV_TILE : 16384 / ROWB;     // tokens of a stage
     constexpr int CPB = 16 * ROWB / 1024;                        // 1 KiB chunks of 16 tokens
     constexpr int NC = ST / 16 * CPB;                            // chunks of K, and of V
@@ -875,15 +895,13 @@ __global__ __launch_bounds__(256, 2) void kv_attention_wide_kernel(KvAttention a
             });
             __builtin_amdgcn_sched_barrier(0);                   // V is read when K is used up
         };
-        auto values = [&](int sb) {
+        auto values = [&](int sb, int v) {
             const uint8_t* vs = sh.kv[1] + (sb * KV_SUB + 4 * g) * ROWB + n * VE * EB;
 #pragma unroll
             for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-#pragma unroll
-                    for (int v = 0; v < VL; ++v)
-                        kv_words<VW, false>(vs + (blk * 16 + r) * ROWB + v * 16 * VE * EB, rows.vf[blk][r][v]);
+                    kv_words<VW, false>(vs + (blk * 16 + r) * ROWB + v * 16 * VE * EB, rows.vf[blk][r][0]);
         };
         while (st < st_end) {
 #pragma unroll 1
@@ -897,7 +915,7 @@ __global__ __launch_bounds__(256, 2) void kv_attention_wide_kernel(KvAttention a
                     scores(s, sb);
                     const bool ok0 = kv_page_of(a, p, t0) < (uint32_t)a.npages;
                     const bool ok1 = kv_page_of(a, p, t0 + 16) < (uint32_t)a.npages;
-                    rows.take_masked(a, p, s, t0, ok0, ok1, lane, [&](bool) { values(sb); });
+                    rows.take_masked(a, p, s, t0, ok0, ok1, lane, [&](int v, bool) { values(sb, v); });
                 }
                 st += ST;
             }
@@ -908,7 +926,7 @@ __global__ __launch_bounds__(256, 2) void kv_attention_wide_kernel(KvAttention a
                 for (int sb = tw; sb < ST / KV_SUB; sb += NTW) {
                     f32x4 s[RB][2];
                     scores(s, sb);
-                    rows.take(p, s, [&] { values(sb); });
+                    rows.take(p, s, [&](int v) { values(sb, v); });
                 }
                 st += ST;
             }
