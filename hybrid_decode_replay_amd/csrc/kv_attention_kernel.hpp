@@ -8,8 +8,9 @@
 // shrink by 2^(old - new).  Partial (m, l, O) of different waves, workgroups and splits join by
 // the same rule; o = O / l, lse = ln 2 (m + log2 l).
 //
-// Bound by HBM: a token's 2 D values serve all rows of its head and are used once, 8 to 64 flop a
-// byte.  So the design keeps loads in flight and the rest out of their way:
+// Bound by HBM: a token's 2 D values serve all rows of its head and are used once, 4 to 64 flop a byte
+// for one token a sequence, against some 300 at which the matrix units would be the limit.  So the
+// design keeps loads in flight and the rest out of their way:
 //
 //  * Scores as S^T = K Q^T and outputs as O^T = V^T P^T on 16x16x32 products.  The result layout of
 //    the first (lane: query row l%16, tokens 4(l/16)..+3 of a 16-token block) is the operand layout
@@ -20,17 +21,23 @@
 //    token.  A lane loads 16 bytes (eight channels) of each of its eight tokens and regroups the
 //    8x8 block with byte permutes: sub-product j takes channel j of every lane's eight, so the
 //    16 lanes of a row load whole rows of V.
-//  * Each wave takes 32 tokens at a time, its K and V in single-buffered registers: the next
-//    tokens' K is requested as soon as the scores are formed and their V as soon as the outputs
-//    are, so 8 to 16 KiB a wave are always on the way and 8 to 16 waves a CU cover the latency.
-//  * Tokens of one page are contiguous; page numbers are wave-uniform and come by scalar loads one
-//    iteration ahead.
-//  * Work is cut evenly, whatever the lengths: the (sequence, head, 128-token tile) units form one
-//    line and workgroup w takes [w N / W, (w + 1) N / W).  Ranges that cover a head alone write its
-//    output; the others leave partial rows that kv_combine_kernel joins.  The line depends on the
-//    lengths alone, so results repeat.
-//  * Weights are carried as two io-type terms (hi + lo, relative 2^-17 for bf16, 2^-22 for fp16):
-//    the products have room to spare, and the output's error stays that of its own rounding.
+//  * Each wave takes 32 tokens at a time, K and V in single-buffered registers: the next tokens' K is
+//    requested as soon as the scores are formed and their V as soon as the outputs are, so 8 to 16 KiB
+//    a wave are always on the way, and eight waves a CU (four where a wave needs more registers) cover
+//    the latency.  Queries stay in LDS for the registers' sake.  Page numbers are wave-uniform and come
+//    by scalar loads one block ahead.
+//  * Work is cut evenly, whatever the lengths: the (sequence, head, 128-token tile) units form one line
+//    and the workgroups take equal stretches of it.  Ranges that a stretch covers write their outputs;
+//    the others leave partial rows that kv_combine_kernel joins.  The line depends on the lengths
+//    alone, so results repeat.  Short ranges (kv_attention_whole) get a workgroup each instead.
+//  * Weights are carried as two io-type terms (hi + lo, relative 2^-16 for bf16, 2^-22 for fp16): one
+//    term alone would double the error of the output's own rounding, and the products have room.
+//  * More than 32 rows of a head (drafts x queries) would make the waves of a workgroup read the cache
+//    again for each other: there it goes through LDS (kv_attention_wide_kernel).
+//
+// Measured with both launches, 537 MB of cache (131k tokens of 8 heads, 128 channels, bf16), read alone
+// in 77 us at the 7.0 TB/s of a plain read: 92 us for 4 rows a head, 94 for 32, 107 for 64, 150 for 128.
+// The same bytes as E4M3 take 97 us, on 64 channels 95, on 256 channels 95 (4 rows a head).
 #pragma once
 #include <type_traits>
 
@@ -116,6 +123,12 @@ __device__ __forceinline__ void kv_words(const uint8_t* p, uint32_t (&w)[N])
     }
 }
 
+// An `end` that the table cannot hold: taken as the nearest that it can.
+__device__ __forceinline__ bool kv_bad_end(const KvAttention& a, int end)
+{
+    return end < 0 || end > (a.max_pages << a.page_shift);
+}
+
 // First and last visible position of a sequence's rows and its tiles.
 struct KvRange {
     int end, base, tiles;
@@ -191,8 +204,9 @@ __device__ __forceinline__ bool kv_line(const KvAttention& a, int* s_pre, int* t
         int v = 0;
         if (b < a.B) {
             const int e = a.end[b];
-            v = kv_range(a, e, !a.active || a.active[b]).tiles * ln.hc;
-            if (blockIdx.x == 0 && a.err && (e < 0 || e > (a.max_pages << a.page_shift))) atomicOr(a.err, KVERR_BAD_SLOT);
+            const bool active = !a.active || a.active[b];
+            v = kv_range(a, e, active).tiles * ln.hc;
+            if (blockIdx.x == 0 && active && a.err && kv_bad_end(a, e)) atomicOr(a.err, KVERR_BAD_SLOT);
         }
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
@@ -235,7 +249,11 @@ struct KvPart {
     float sc;                                // signed scale of the raw products, in powers of two
     __device__ __forceinline__ bool whole() const { return ta == 0 && tb == tiles; }
     // (a scale of zero would let masked scores through: the smallest normal number stands for it)
-    __device__ __forceinline__ float sc_abs() const { return fmaxf(__builtin_fabsf(sc), 0x1p-126f); }
+    __device__ __forceinline__ float sc_abs() const
+    {
+        const float x = __builtin_fabsf(sc);
+        return x < 0x1p-126f ? 0x1p-126f : x;
+    }
     // every row sees every one of the n tokens at t
     __device__ __forceinline__ bool full(int t, int n) const { return t >= all_lo && t + n <= all_hi; }
 };
@@ -278,7 +296,7 @@ __device__ __forceinline__ bool kv_whole_part(const KvAttention& a, KvPart& p)
     const int hc = a.Hkv * a.nchunk, b = uni(blockIdx.x / hc), seg = uni(blockIdx.x - b * hc);
     if (a.active && !uload(a.active + b)) return false;
     const int e = uload(a.end + b);
-    if (seg == 0 && threadIdx.x == 0 && a.err && (e < 0 || e > (a.max_pages << a.page_shift))) atomicOr(a.err, KVERR_BAD_SLOT);
+    if (seg == 0 && threadIdx.x == 0 && a.err && kv_bad_end(a, e)) atomicOr(a.err, KVERR_BAD_SLOT);
     const KvRange rng = kv_range(a, e, true);
     p = kv_part<FP8>(a, b, rng, seg, 0, rng.tiles);
     return true;

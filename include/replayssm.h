@@ -423,7 +423,9 @@ replay_status replay_standin_attention(const void *q, int64_t q_stride, const vo
  *   then             stack of free pages [npages], the next one at the top
  * All of it changes on the device only, in stream order, so a captured graph
  * of a decode step can cross page boundaries.  Results depend on the calls made
- * and their arguments alone (no atomics decide an order). */
+ * and their arguments alone (no atomics decide an order).  Arrays of words (per
+ * sequence or per row) need only their element's alignment, so they may be
+ * slices; q, k, v, K, V and outputs need 16 bytes, regions and workspaces 256. */
 typedef struct {
     int32_t abi_version;  /* REPLAY_ABI_VERSION                                    */
     int32_t batch;        /* B in [1, 4096]                                        */
@@ -438,8 +440,9 @@ typedef struct {
 #define REPLAY_KVERR_TOO_LONG 0x2u   /* reserve: more tokens than max_pages hold, a negative
                                         count, or rows past the arrays               */
 #define REPLAY_KVERR_BAD_SLOT 0x4u   /* append: a slot outside the cache (row skipped);
-                                        attention: a page outside it, or an `end` past the
-                                        table (those positions are masked)           */
+                                        attention: a page outside it (those positions
+                                        are masked), or an `end` that is negative or
+                                        past the table (taken as the nearest that fits) */
 #define REPLAY_KVERR_CLAMPED  0x8u   /* commit: a count outside [0, end - len]       */
 
 /* Bytes of the pool's region (0 if the configuration is invalid).  The region
