@@ -194,3 +194,46 @@ def test_joined_results_repeat_on_a_graph():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(o, want)
+
+
+@pytest.mark.parametrize("group,T,D", [(2, 1, 64), (13, 5, 64), (13, 5, 256)])
+def test_the_largest_batch(group, T, D):
+    """4096 sequences: every seventh holds something; and once with all but one idle."""
+    lens = [(b * 5) % 33 if b % 7 == 0 else 0 for b in range(4096)]
+    p = problem(lens, group, 1, D, 16, T, BF, False, 95, max_pages=161)
+    verify(p)
+    want, wl = call(p, D ** -0.5)
+    active = torch.zeros(4096, dtype=torch.uint8, device="cuda")
+    active[2800] = 1
+    got, gl = call(p, D ** -0.5, active=active, o=torch.full_like(want, 3.0))
+    assert torch.equal(got[:, 2800], want[:, 2800]) and torch.equal(gl[:, 2800], wl[:, 2800])
+    assert (got[:, :2800] == 3.0).all() and (got[:, 2801:] == 3.0).all()
+
+
+@pytest.mark.parametrize("max_pages", [20, 200])
+@pytest.mark.parametrize("group,T", [(4, 1), (16, 4)])
+def test_infinite_scores(group, T, max_pages):
+    """A key whose score is -inf weighs nothing, also where whole blocks of them come first; one of
+    +inf leaves no number, in the rows that see it."""
+    p = problem([300, 40], group, 1, 128, 16, T, BF, False, 61, max_pages=max_pages)
+    p["q"].view(-1, 128)[:, 9] = -1.0
+    rows = p["table"][0, :19].long()
+    gone = list(range(0, 200)) + [250]
+    K = p["K"].clone()
+    for j in gone:
+        K[rows[j // 16], 0, j % 16, 9] = float("inf")
+    got, lse = call(dict(p, K=K), 0.09)
+    # the same positions with keys that weigh 2^-200 or less: 0.09 * 3e4 is 2700 below the others
+    far = p["K"].clone()
+    for j in gone:
+        far[rows[j // 16], 0, j % 16, 9] = 3e4
+    ro, rl, top, a = reference(dict(p, K=far), 0.09)
+    clean = reference(p, 0.09)
+    check_attention(got, lse, (ro, rl, clean[2], a), 128, 4 * 300, BF)
+    K = p["K"].clone()
+    K[rows[298 // 16], 0, 298 % 16, 9] = float("-inf")
+    got, _ = call(dict(p, K=K), 0.09)
+    want, _ = call(p, 0.09)
+    first = max(0, T - 2)                                   # position 298 is seen by the last two drafts
+    assert torch.isnan(got[first:, 0]).all() and torch.equal(got[:, 1], want[:, 1])
+    assert torch.equal(got[:first, 0], want[:first, 0])
