@@ -34,8 +34,9 @@ KvPlan kv_attention_plan(int D, bool fp8, int rows)
 
 // Splitting evens the work out but costs a second launch and the partial rows (about 12 us); a
 // workgroup per range costs the wait for the longest one.  Measured: drafts in a window of 1024 tokens
-// 34 us split, 19 whole; 2048 ranges of up to 2001 tokens 126 and 114; 512 ranges of up to 4097 tokens
-// 120 and 142.
+// 34 us split, 19 whole; 2048 ranges of up to 2001 tokens 126 split, 114 whole, 104 to 108 whole with the
+// longest first; 512 ranges of up to 4097 tokens 120 split, 142 whole.  What the lengths themselves say
+// is weighed in the kernel (kv_order).
 bool kv_attention_whole(long long tokens, long long ranges)
 {
     return ranges < (1 << 22) && (tokens <= 1280 || (tokens <= 2560 && ranges >= 2048));
@@ -1373,7 +1374,11 @@ replay_status replay_kv_attention(const replay_kv_layer* layer, const replay_kv_
     a.nchunk = p.nchunk;
     // the most tokens a sequence's rows can see, in blocks of 32
     const long long cap = (long long)x.max_pages * layer->page_size, seen = (long long)a.window + x.ntok - 1 + 31;
-    a.whole = rs::kv_attention_whole(a.window > 0 && seen < cap ? seen : cap, (long long)x.batch * Hkv * p.nchunk);
+    // (short ranges are over sooner than their order is found: 2048 of 200 tokens 47 us as they stand, 58 by length)
+    const long long most = a.window > 0 && seen < cap ? seen : cap, ranges = (long long)x.batch * Hkv * p.nchunk;
+    a.whole = rs::kv_attention_whole(most, ranges);
+    a.by_length = most > 1280 && ranges > p.nwg && ranges < (1 << 22) && x.batch <= rs::KV_BY_LENGTH;
+    a.nwg = p.nwg;
     a.scale_log2 = (float)((double)x.scale * 1.4426950408889634);
     const bool bf = layer->io_dtype == REPLAY_BF16, fp8 = layer->cache_dtype == REPLAY_FP8_E4M3;
     const auto run = bf ? (fp8 ? rs::launch_kv_attention_bf16_fp8 : rs::launch_kv_attention_bf16)

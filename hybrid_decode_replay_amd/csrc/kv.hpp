@@ -59,6 +59,8 @@ struct KvAttention {
     int rpc;                 // rows of a chunk, at most 16 RB RW
     int nchunk;              // chunks of rows
     bool whole;              // a workgroup per range, nothing to join
+    bool by_length;          // a workgroup per range, the longest first: if whole, or if that is even enough
+    int nwg;                 // workgroups of the line
     float scale_log2;        // scale * log2(e)
 };
 // How a call is cut: row blocks of 16 per wave, row groups (more than one in the wide kernel), rows
@@ -76,6 +78,7 @@ constexpr int kv_occ(int D, bool fp8, int RB)
     return D == 256 || (D == 128 && RB == 2 && !fp8) ? 1 : 2;
 }
 KvPlan kv_attention_plan(int D, bool fp8, int rows);
+constexpr int KV_BY_LENGTH = 1024;       // sequences that can be taken in the order of their lengths
 // Whether ranges of at most `tokens` tokens are short enough for a workgroup each.
 bool kv_attention_whole(long long tokens, long long ranges);
 // One translation unit per io and cache type.

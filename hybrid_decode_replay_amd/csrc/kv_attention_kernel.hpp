@@ -29,7 +29,8 @@
 //  * Work is cut evenly, whatever the lengths: the (sequence, head, 128-token tile) units form one line
 //    and the workgroups take equal stretches of it.  Ranges that a stretch covers write their outputs;
 //    the others leave partial rows that kv_combine_kernel joins.  The line depends on the lengths
-//    alone, so results repeat.  Short ranges (kv_attention_whole) get a workgroup each instead.
+//    alone, so results repeat.  Ranges known to be short (kv_attention_whole) and many ranges of like
+//    lengths (kv_order) get a workgroup each instead.
 //  * Weights are carried as two io-type terms (hi + lo, relative 2^-16 for bf16, 2^-22 for fp16): one
 //    term alone would double the error of the output's own rounding, and the products have room.
 //  * More than 32 rows of a head (drafts x queries) would make the waves of a workgroup read the cache
@@ -187,7 +188,7 @@ struct KvGeom {
 // The line of units as a workgroup sees it, and its place on it.
 struct KvLine {
     int hc, u, u1, b;                        // ranges per sequence; first and last + 1 unit; sequence of the first
-    bool by_range;
+    bool by_range, whole;
     KvCut cut;
 };
 
@@ -198,6 +199,7 @@ __device__ __forceinline__ bool kv_line(const KvAttention& a, int* s_pre, int* t
 {
     const int tid = threadIdx.x, lane = tid & 63, wv = uni(tid >> 6);
     ln.hc = a.Hkv * a.nchunk;
+    ln.whole = false;
     int carry = 0;
     for (int b0 = 0; b0 < a.B; b0 += NT) {
         const int b = b0 + tid;
@@ -226,8 +228,8 @@ __device__ __forceinline__ bool kv_line(const KvAttention& a, int* s_pre, int* t
         __syncthreads();
     }
     // at most a unit each, so that no workgroup inside a split range is without one
-    const int N = uni(s_pre[a.B]), W = min((int)gridDim.x, N);
-    ln.by_range = a.B * ln.hc <= (int)gridDim.x;
+    const int N = uni(s_pre[a.B]), W = min(a.nwg, N);
+    ln.by_range = a.B * ln.hc <= a.nwg;
     if (!ln.by_range && tid == 0) a.meta[2 * blockIdx.x] = -1;
     if ((int)blockIdx.x >= W) return false;
     const int each = uni(N / W);
@@ -279,27 +281,105 @@ __device__ __forceinline__ KvPart kv_part(const KvAttention& a, int b, const KvR
     p.sc = FP8 ? a.scale_log2 * uload(a.k_scale + p.hkv) : a.scale_log2;
     return p;
 }
-// The next part of a workgroup's stretch of the line.
-template <bool FP8>
-__device__ __forceinline__ KvPart kv_line_part(const KvAttention& a, const int* s_pre, KvLine& ln)
+// Where there are more ranges than the chip holds workgroups: whether each takes a range of its own, the
+// longest first so that the last ones are short, and which.  Even shares need no join then; but a range
+// longer than an even share would outlast the others, so with one such the line is cut instead.  Every
+// wave finds it for itself: the tiles of the batch in N registers (at least B / 64), the length of the
+// range at place `at` by bisection, counting with ballots (lengths in 32 steps, equal ones as they stand).
+// Lengths of 64 to 4000, 128 channels, 8 heads, tables of 32768 tokens, E4M3: 128 sequences 122 us on the
+// line, 100 by length, 256 sequences 210 and 182; the same with all but one sequence eight times shorter
+// (on the line): 43 us without this choice, 44 with it, and 67 and 69.
+struct KvOrder {
+    bool whole;
+    int b;
+};
+template <int N>
+__device__ __forceinline__ KvOrder kv_order(const KvAttention& a, int at)
 {
-    while (uni(s_pre[ln.b + 1]) <= ln.u) ++ln.b;
-    const int b = uni(ln.b), at = ln.u - uni(s_pre[b]);
-    const KvRange rng = kv_range(a, uload(a.end + b), true);
-    const int seg = at / rng.tiles, ta = at - seg * rng.tiles;
-    return kv_part<FP8>(a, b, rng, seg, ta, min(rng.tiles, ta + ln.u1 - ln.u));
+    const int lane = threadIdx.x & 63;
+    int tiles[N], most = 0, sum = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int b = i * 64 + lane;
+        tiles[i] = -1;
+        if (b < a.B) {
+            tiles[i] = kv_range(a, a.end[b], !a.active || a.active[b]).tiles;
+            most = max(most, tiles[i]);
+            sum += tiles[i];
+        }
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        most = max(most, __shfl_xor(most, o, 64));
+        sum += __shfl_xor(sum, o, 64);
+    }
+    most = uni(most);
+    KvOrder r;
+    r.whole = a.whole || (long long)most * a.nwg <= (long long)uni(sum) * (a.Hkv * a.nchunk);
+    r.b = 0;
+    if (!r.whole) return r;
+    const int shift = max(0, 27 - __builtin_clz(most | 1));      // most >> shift is below 32
+#pragma unroll
+    for (int i = 0; i < N; ++i) tiles[i] >>= shift;
+    auto as_long = [&](int n) {
+        int c = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) c += __builtin_popcountll(__builtin_amdgcn_ballot_w64(tiles[i] >= n));
+        return c;
+    };
+    int n = 0, left = at;                             // left: places after the longer ones
+#pragma unroll
+    for (int bit = 16; bit > 0; bit >>= 1) {
+        const int c = as_long(n + bit);
+        if (c > at) n += bit;
+        else left = at - c;                           // (the last such count is that of n + 1)
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint64_t same = __builtin_amdgcn_ballot_w64(tiles[i] == n);
+        const int c = __builtin_popcountll(same);
+        if (left >= 0 && left < c) {
+            const bool it = tiles[i] == n && (int)__builtin_popcountll(same & ((1ull << lane) - 1)) == left;
+            r.b = i * 64 + __builtin_ctzll(__builtin_amdgcn_ballot_w64(it));
+        }
+        left -= c;
+    }
+    r.b = uni(r.b);
+    return r;
 }
-// Range blockIdx.x as one part (calls without a line); false for an idle sequence.
-template <bool FP8>
-__device__ __forceinline__ bool kv_whole_part(const KvAttention& a, KvPart& p)
+// This workgroup's place on the line, or its range (ln.whole: u is its head and chunk); false if it has
+// neither.
+__device__ __forceinline__ bool kv_begin(const KvAttention& a, int* s_pre, int* tmp, KvLine& ln)
 {
-    const int hc = a.Hkv * a.nchunk, b = uni(blockIdx.x / hc), seg = uni(blockIdx.x - b * hc);
+    const int hc = a.Hkv * a.nchunk, at = uni(blockIdx.x / hc), seg = uni(blockIdx.x - at * hc);
+    int b = at;
+    bool whole = a.whole;
+    if (a.by_length) {
+        const KvOrder o = a.B <= 256 ? kv_order<4>(a, at) : kv_order<KV_BY_LENGTH / 64>(a, at);
+        whole = o.whole;
+        b = o.b;
+        if (!whole && (int)blockIdx.x >= a.nwg) return false;
+        if (whole && !a.whole && (int)blockIdx.x < a.nwg && threadIdx.x == 0) a.meta[2 * blockIdx.x] = -1;
+    }
+    if (!whole) return kv_line<256>(a, s_pre, tmp, ln);
+    ln.whole = true;
+    ln.b = b;
+    ln.u = seg;
+    ln.u1 = seg + 1;
     if (a.active && !uload(a.active + b)) return false;
-    const int e = uload(a.end + b);
-    if (seg == 0 && threadIdx.x == 0 && a.err && kv_bad_end(a, e)) atomicOr(a.err, KVERR_BAD_SLOT);
-    const KvRange rng = kv_range(a, e, true);
-    p = kv_part<FP8>(a, b, rng, seg, 0, rng.tiles);
+    if (seg == 0 && threadIdx.x == 0 && a.err && kv_bad_end(a, uload(a.end + b))) atomicOr(a.err, KVERR_BAD_SLOT);
     return true;
+}
+// Its next part.
+template <bool FP8>
+__device__ __forceinline__ KvPart kv_next_part(const KvAttention& a, const int* s_pre, KvLine& ln)
+{
+    if (!ln.whole)
+        while (uni(s_pre[ln.b + 1]) <= ln.u) ++ln.b;
+    const int b = uni(ln.b), u = uni(ln.u), at = ln.whole ? 0 : uni(u - s_pre[b]);
+    const KvRange rng = kv_range(a, uload(a.end + b), true);
+    const int seg = ln.whole ? u : at / rng.tiles, ta = ln.whole ? 0 : at - seg * rng.tiles;
+    return kv_part<FP8>(a, b, rng, seg, ta, ln.whole ? rng.tiles : min(rng.tiles, ta + ln.u1 - u));
 }
 
 // Whether a table entry of the part lies outside the cache (its blocks then take the masked path).
@@ -708,11 +788,10 @@ __global__ __launch_bounds__(256, OCC) void kv_attention_kernel(KvAttention a)
     __shared__ int s_wave[4];
     const int lane = threadIdx.x & 63, wv = uni(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
     KvLine ln;
-    KvPart p;
-    if (a.whole ? !kv_whole_part<FP8>(a, p) : !kv_line<256>(a, s_pre, s_wave, ln)) return;
+    if (!kv_begin(a, s_pre, s_wave, ln)) return;
 #pragma unroll 1
-    while (a.whole || ln.u < ln.u1) {
-        if (!a.whole) p = kv_line_part<FP8>(a, s_pre, ln);
+    while (ln.u < ln.u1) {
+        const KvPart p = kv_next_part<FP8>(a, s_pre, ln);
         R rows;
         rows.init();
         constexpr int step = 4 * KV_SUB;
@@ -816,7 +895,7 @@ __global__ __launch_bounds__(256, OCC) void kv_attention_kernel(KvAttention a)
             if (!taken) masked(std::false_type{});
         }
         rows.template join<256, 1, 4, JP>(a, p, sh.o, s_m, s_l);
-        if (a.whole) break;
+        if (ln.whole) break;
         kv_next(a, p, s_pre, ln);
     }
 }
@@ -853,8 +932,7 @@ __global__ __launch_bounds__(256, 2) void kv_attention_wide_kernel(KvAttention a
     __shared__ int s_wave[4];
     const int lane = threadIdx.x & 63, wv = uni(threadIdx.x >> 6), rg = wv % RW, tw = wv / RW, n = lane & 15, g = lane >> 4;
     KvLine ln;
-    KvPart p;
-    if (a.whole ? !kv_whole_part<FP8>(a, p) : !kv_line<256>(a, s_pre, s_wave, ln)) return;
+    if (!kv_begin(a, s_pre, s_wave, ln)) return;
     // chunk j of a wave is chunk wv + 4 j of the stage: block, and the lane's bytes in the block
     auto block_of = [&](int j) { return (wv + 4 * j) / CPB; };
     uint32_t koff[CV], voff[CV];
@@ -865,8 +943,8 @@ __global__ __launch_bounds__(256, 2) void kv_attention_wide_kernel(KvAttention a
         koff[c] = tok * ROWB + (pos ^ ((tok / FT) & FM)) * 16;
     }
 #pragma unroll 1
-    while (a.whole || ln.u < ln.u1) {
-        if (!a.whole) p = kv_line_part<FP8>(a, s_pre, ln);
+    while (ln.u < ln.u1) {
+        const KvPart p = kv_next_part<FP8>(a, s_pre, ln);
         R rows;
         rows.init();
         const uint8_t* Kc = static_cast<const uint8_t*>(a.K);
@@ -952,7 +1030,7 @@ __global__ __launch_bounds__(256, 2) void kv_attention_wide_kernel(KvAttention a
             }
         }
         rows.template join<256, RW, NTW, JP>(a, p, sh.o, s_m, s_l);
-        if (a.whole) break;
+        if (ln.whole) break;
         kv_next(a, p, s_pre, ln);
     }
 }
@@ -1039,7 +1117,7 @@ static hipError_t kv_attention_width(const KvAttention& a, const KvPlan& p, hipS
 {
     const int ranges = a.B * a.Hkv * a.nchunk;
     const size_t lds = a.whole ? 0 : (a.B + 1) * sizeof(int);
-    const dim3 grid(a.whole ? ranges : p.nwg);
+    const dim3 grid(a.whole || a.by_length ? ranges : p.nwg);
     if (p.wide) {
         if constexpr (D == 256) {
             hipLaunchKernelGGL((kv_attention_wide_kernel<IO, FP8, D, 1, 4>), grid, dim3(256), lds, s, a);

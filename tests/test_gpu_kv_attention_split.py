@@ -237,3 +237,54 @@ def test_infinite_scores(group, T, max_pages):
     first = max(0, T - 2)                                   # position 298 is seen by the last two drafts
     assert torch.isnan(got[first:, 0]).all() and torch.equal(got[:, 1], want[:, 1])
     assert torch.equal(got[:first, 0], want[:first, 0])
+
+
+@pytest.mark.parametrize("max_pages", [160, 200])
+@pytest.mark.parametrize("B,Hkv,group,T,D", [(700, 3, 2, 1, 64), (250, 9, 2, 2, 64), (1024, 2, 12, 4, 64), (70, 8, 3, 1, 256)])
+def test_the_longest_first(B, Hkv, group, T, D, max_pages):
+    """More ranges than workgroups, none longer than an even share: a workgroup each, by length."""
+    r = rng(B, D)
+    lens = [int(n) for n in r.integers(0, 300 if B < 1000 else 100, B)]
+    lens[-1], lens[0] = 0, 3
+    p = problem(lens, Hkv * group, Hkv, D, 16, T, BF, False, 97, max_pages=max_pages)
+    verify(p)
+    want, wl = call(p, D ** -0.5)
+    on = r.integers(0, 5, B) > 0
+    active = torch.from_numpy(on.astype(np.uint8)).cuda()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got, gl = call(p, D ** -0.5, active=active, o=torch.full_like(want, 3.0), err=err)
+    on = torch.from_numpy(on).cuda()
+    assert torch.equal(got[:, on], want[:, on]) and torch.equal(gl[:, on], wl[:, on]) and int(err) == 0
+    assert (got[:, ~on] == 3.0).all() and (gl[:, ~on] == 7.0).all()
+    p["end"][B // 2] = 2 ** 31 - 1
+    p["end"][B // 3] = -5
+    call(p, D ** -0.5, err=err)
+    assert int(err) == 4
+
+
+def test_even_and_uneven_lengths_on_one_graph():
+    """The cut follows the lengths that a replay finds: even ones, one long one, none."""
+    from hybrid_decode_replay_amd import binding as rb
+    full = [60] * 299 + [2900]
+    p = problem(full, 4, 2, 64, 16, 1, BF, False, 54, max_pages=190)
+    c = lambda n: p[n].cuda()  # noqa: E731
+    q, K, V, table, end = c("q"), c("K"), c("V"), c("table"), c("end")
+    ws = torch.zeros(rb.kv_attention_workspace(p["layer"], 300), dtype=torch.uint8, device="cuda")
+    o = torch.zeros((1, 300, 4, 64), dtype=BF, device="cuda")
+    run = lambda: rb.kv_attention(p["layer"], q, K, V, table, end, ws=ws, o=o)  # noqa: E731
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        run()
+    torch.cuda.current_stream().wait_stream(st)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    for last in (2900, 60, 0, 2900, 61):
+        end.copy_(torch.tensor([60] * 299 + [last], dtype=torch.int32))
+        o.fill_(5.0)
+        g.replay()
+        torch.cuda.synchronize()
+        p["end"] = end.cpu()
+        ref = reference(p, 64 ** -0.5)
+        check_attention(o, None, ref, 64, 2900, BF)
