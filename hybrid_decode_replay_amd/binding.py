@@ -808,6 +808,7 @@ def kv_attention(layer: KVLayer, q, K, V, table, end, ntok=1, scale=None, window
     shape = (layer.npages, Hkv, layer.page_size, D)
     if table.dim() != 2:
         raise ValueError("table must be [B][max_pages]")
+    window = max(-1, min(window, (1 << 31) - 1))     # (past every position: all of them)
     mp = table.shape[1]
     if o is None:
         o = torch.zeros((ntok, B, H, D), dtype=io, device=dev)

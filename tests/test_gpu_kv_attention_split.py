@@ -288,3 +288,18 @@ def test_even_and_uneven_lengths_on_one_graph():
         p["end"] = end.cpu()
         ref = reference(p, 64 ** -0.5)
         check_attention(o, None, ref, 64, 2900, BF)
+
+
+def test_windows_past_every_position_are_none():
+    import sys
+
+    from hybrid_decode_replay_amd import binding as rb
+    p = problem([300, 41], 4, 2, 64, 16, 2, BF, False, 98)
+    want, wl = call(p, 0.125)
+    for window in (20 * 16, 2 ** 31 - 1, 2 ** 32 + 5, sys.maxsize):
+        got, gl = call(p, 0.125, window)
+        assert torch.equal(got, want) and torch.equal(gl, wl)
+    for window in (-1, -2 ** 32 + 5):
+        with pytest.raises(rb.ReplayError) as e:
+            call(p, 0.125, window)
+        assert e.value.status == rb.ERR_ARG
