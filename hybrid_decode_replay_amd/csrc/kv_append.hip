@@ -10,7 +10,8 @@
 // its angle to 10^-9), the fraction goes to sincospi in fp32.
 //
 // Bound by HBM: q, k and v are read once and written once.  16387 rows of 32 + 2 x 8 heads of 128
-// channels, 403 MB: 73 us, 5.5 TB/s, against 5.9 TB/s of a copy.
+// channels, 403 MB: 73 us, 5.5 TB/s, against 5.9 TB/s of a copy.  1024 rows on an E4M3 cache 6.2 us, one
+// row 2.8 (launch and three dependent loads).
 #include <type_traits>
 
 #include "kv_io.hpp"
