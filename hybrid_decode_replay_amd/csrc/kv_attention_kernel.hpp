@@ -382,11 +382,14 @@ __device__ __forceinline__ KvPart kv_next_part(const KvAttention& a, const int* 
     return kv_part<FP8>(a, b, rng, seg, ta, ln.whole ? rng.tiles : min(rng.tiles, ta + ln.u1 - u));
 }
 
-// Whether a table entry of the part lies outside the cache (its blocks then take the masked path).
+// Whether a table entry that some row of the part sees lies outside the cache (the part's blocks then
+// take the masked path).  Pages before the first visible position, which may share a block with it,
+// are nobody's: a window's table may have dropped them.
 __device__ __forceinline__ bool kv_wrong_pages(const KvAttention& a, const KvPart& p, int lane)
 {
     bool wrong = false;
-    for (int i = ((p.base + p.ta * KV_TILE) >> a.page_shift) + lane;
+    const int lo = a.window > 0 ? max(0, p.end - a.T - a.window + 1) : 0;
+    for (int i = (max(p.base + p.ta * KV_TILE, lo) >> a.page_shift) + lane;
          i < (p.tend + (1 << a.page_shift) - 1) >> a.page_shift; i += 64)
         wrong |= (uint32_t)p.table[i] >= (uint32_t)a.npages;
     wrong = __builtin_amdgcn_ballot_w64(wrong) != 0;

@@ -440,8 +440,8 @@ typedef struct {
 #define REPLAY_KVERR_TOO_LONG 0x2u   /* reserve: more tokens than max_pages hold, a negative
                                         count, or rows past the arrays               */
 #define REPLAY_KVERR_BAD_SLOT 0x4u   /* append: a slot outside the cache (row skipped);
-                                        attention: a page outside it (those positions
-                                        are masked), or an `end` that is negative or
+                                        attention: a visible page outside it (those
+                                        positions are masked), or an `end` that is negative or
                                         past the table (taken as the nearest that fits) */
 #define REPLAY_KVERR_CLAMPED  0x8u   /* commit: a count outside [0, end - len]       */
 
@@ -546,6 +546,7 @@ size_t replay_kv_attention_workspace(const replay_kv_layer *layer, int32_t batch
 /* Attention of the last ntok tokens of every sequence over its cache: token t
  * of sequence b is at position p = end[b] - ntok + t and, for head h,
  *   o = sum_j w_j V_j,  w = softmax of scale * q.K_j  over max(0, p - window + 1) <= j <= p.
+ * Table entries of pages that no token sees (behind end, before the windows) do not matter.
  * A token that sees nothing (p < 0, or only positions without a page) gives
  * o = 0 and lse = -inf.  What lies in masked positions does not matter, NaN
  * included.  Softmax statistics and sums are fp32; weights are carried in two
