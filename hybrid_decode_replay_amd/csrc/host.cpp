@@ -1278,7 +1278,8 @@ replay_status replay_kv_append(const replay_kv_layer* layer, const replay_kv_app
     if (!args) return fail(REPLAY_ERR_ARG, "append arguments are NULL");
     const replay_kv_append_args& x = *args;
     const int Hq = layer->nheads, Hkv = layer->nkv, D = layer->head_dim;
-    if (x.rows < 0 || x.rows > (1 << 25)) return fail(REPLAY_ERR_SHAPE, "rows %d outside [0, 2^25]", x.rows);
+    // (two rows a workgroup of 256 lanes, and a launch holds less than 2^32 of them)
+    if (x.rows < 0 || x.rows > (1 << 25) - 2) return fail(REPLAY_ERR_SHAPE, "rows %d outside [0, 2^25 - 2]", x.rows);
     if ((s = check_ptr(x.K, "K")) != REPLAY_OK) return s;
     if ((s = check_ptr(x.V, "V")) != REPLAY_OK) return s;
     if ((s = check_kv_scales(layer, x.k_scale, x.v_scale)) != REPLAY_OK) return s;

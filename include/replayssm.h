@@ -507,7 +507,7 @@ typedef struct {
     const uint8_t *axis;          /* [rot_dim / 2] axis of each pair, NULL = 0; a pair whose
                                      axis is >= naxes turns by 0                    */
     int32_t naxes;                /* 1..8                                           */
-    int32_t rows;                 /* >= 0                                           */
+    int32_t rows;                 /* 0..2^25 - 2                                    */
     void *q_out;                  /* [rows][Hq*D] io_dtype; with q only             */
     void *K, *V;                  /* the layer's cache                              */
     const float *k_scale, *v_scale;   /* [Hkv], FP8 cache only                      */
