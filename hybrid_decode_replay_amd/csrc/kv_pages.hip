@@ -171,14 +171,20 @@ __global__ __launch_bounds__(256) void kv_fill_kernel(KvPool p, int rows, int64_
     int32_t* row = p.table + (size_t)b * p.max_pages;
     const int32_t* top = p.free + (nfree - 1 - first);
     for (int i = t0; i < got; i += step) row[H + i] = top[-i];
-    for (int i = t0; i < n; i += step) {
-        const long long r = (long long)start + i;
-        if (r >= rows) break;
-        const int q = L + i, pi = q >> p.page_shift;
+    // rows of the sequence within the arrays; counted in 64 bits, since a count may be 2^31 - 1 (not
+    // served, but its rows are marked)
+    const long long most = min((long long)n, (long long)rows - start);
+    for (long long i = t0; i < most; i += step) {
+        const long long r = start + i;
         int64_t slot = -1;
-        if (given) slot = ((int64_t)(pi < H ? row[pi] : top[-(pi - H)]) << p.page_shift) + (q & (ps - 1));
+        int q = -1;
+        if (given) {
+            q = L + (int)i;
+            const int pi = q >> p.page_shift;
+            slot = ((int64_t)(pi < H ? row[pi] : top[-(pi - H)]) << p.page_shift) + (q & (ps - 1));
+        }
         slots[r] = slot;
-        pos[r] = given ? q : -1;
+        pos[r] = q;
     }
 }
 
