@@ -744,6 +744,11 @@ class KVPages:
                 _addr(starts, dev, torch.int32, "starts", (B + 1,)))
         return (slots, pos) if counts is None else (slots, pos, starts)
 
+    def served(self):
+        """The sequences with new tokens in the open step (device uint8 [B]): the `active` of its attention
+        and of the replayed states' step.  Idle ones and those that reserve refused are 0."""
+        return (self.end > self.len).to(_torch().uint8)
+
     def commit(self, accepted=None):
         """Keeps accepted[b] (device int32 [B], None = all) of the open step's tokens."""
         _launch(self.device, "replay_kv_commit", _lib.replay_kv_commit, *self._mem(),

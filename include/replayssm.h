@@ -466,7 +466,11 @@ replay_status replay_kv_reset(const replay_kv_config *cfg, void *mem, void *stre
  * slots (device int64 [rows]) and pos (device int32 [rows]) receive every row's
  * slot and position, -1 for the rows of a sequence that was not served and for
  * rows without a token.  A second reserve before a commit opens the step anew;
- * pages already held are kept. */
+ * pages already held are kept.
+ * A sequence that was not served has no new token, and end[b] == len[b]: append
+ * skips its rows (q_out keeps what it held), and attention would take its last
+ * kept tokens for the new ones.  The mask of the served, end[b] > len[b], is the
+ * `active` of the step's attention, and of the replayed states' step. */
 replay_status replay_kv_reserve(const replay_kv_config *cfg, void *mem, int32_t ntok, const int32_t *counts,
                                 const uint8_t *active, int32_t rows, int64_t *slots, int32_t *pos, int32_t *starts,
                                 void *stream);
