@@ -32,14 +32,31 @@ KvPlan kv_attention_plan(int D, bool fp8, int rows)
     return p;
 }
 
-// Splitting evens the work out but costs a second launch and the partial rows (about 12 us); a
-// workgroup per range costs the wait for the longest one.  Measured: drafts in a window of 1024 tokens
-// 34 us split, 19 whole; 2048 ranges of up to 2001 tokens 126 split, 114 whole, 104 to 108 whole with the
-// longest first; 512 ranges of up to 4097 tokens 120 split, 142 whole.  What the lengths themselves say
-// is weighed in the kernel (kv_order).
-bool kv_attention_whole(long long tokens, long long ranges)
+// Whether each range takes a workgroup of its own, with nothing to join, from what the host knows: the
+// most tokens a range can have (the table's or the window's), not the lengths.  Times in us:
+//   alone   the longest range in one workgroup.  A workgroup reads 40 GB/s (256 bytes a token 6.6 us per
+//           1024 tokens, 512 bytes 12.4, 1024 bytes 25); through LDS it is the work that counts, 21 us per
+//           1024 tokens of 128 channels and 42 of 256, for E4M3 too.
+//   join    what a split adds: the second launch, and its rows (one range 5 us on the device, 192 ranges of
+//           4 rows 6, of 32 rows 15, of 64 rows 24), and up to 2.5 us of the host's, which is what small
+//           calls wait for that are not captured.
+//   even    what a split takes at least: a tile in each workgroup, or all ranges at the chip's rate.
+// The rows and the third count up to 20 and 8 us, since ranges may be much shorter than they can be, and the
+// chip then waits for the one that is not.
+// Measured with a cold cache, whole / split: one range of 256 tokens 5.9 / 10.1 (D 64), 8.9 / 11.6 (128), 13.4 /
+// 14.9 (256), of 1024 11.0 / 10.3, 18.2 / 11.7, 32 / 15; 192 ranges of 2048 tokens 24.0 / 28.5, 41 / 44, 77 / 76,
+// with 32 rows of a head 26.5 / 41.4, 45 / 57, 85 / 103; 504 ranges of up to 2048 tokens (D 64) 37 / 45, one of
+// 2048 among others of 128 21 / 17.  Over 1037 such calls (widths, types, 4 to 128 rows, 1 to 6400 ranges; even
+// lengths, a ramp, one long one) the rule costs 2, 5 and 8 % against the better choice, 1.9 times at worst;
+// limits of tokens alone cost 5, 8 and 9, and 2.5 times.  What the lengths themselves say is weighed in
+// the kernel where there are more ranges than workgroups (kv_order).
+bool kv_attention_whole(const KvPlan& p, int D, bool fp8, long long tokens, long long ranges)
 {
-    return ranges < (1 << 22) && (tokens <= 1280 || (tokens <= 2560 && ranges >= 2048));
+    const double bytes = 2.0 * D * (fp8 ? 1 : 2), token = p.wide ? 160e-6 * D : bytes / 40e3;
+    const double alone = tokens * token, split = (double)(ranges < p.nwg ? ranges : p.nwg);
+    const double rows = split * p.rpc / 400, join = 7.5 + (rows < 20 ? rows : 20);
+    const double all = ranges * tokens * bytes / 5.9e6, even = all < 8 ? all : 8, tile = 128 * token;
+    return ranges < (1 << 22) && alone <= join + (even > tile ? even : tile);
 }
 
 }  // namespace rs
@@ -1326,6 +1343,7 @@ replay_status replay_kv_attention(const replay_kv_layer* layer, const replay_kv_
     replay_status s = check_kv_call(layer, x.batch, x.ntok, &p);
     if (s != REPLAY_OK) return s;
     const int Hq = layer->nheads, Hkv = layer->nkv, D = layer->head_dim;
+    const bool fp8 = layer->cache_dtype == REPLAY_FP8_E4M3;
     if ((s = check_kv_table(x.batch, x.max_pages, layer->page_size)) != REPLAY_OK) return s;
     if ((s = check_ptr(x.q, "q")) != REPLAY_OK) return s;
     if ((s = check_row_stride(x.q_stride, (long long)Hq * D, "q_stride")) != REPLAY_OK) return s;
@@ -1377,11 +1395,11 @@ replay_status replay_kv_attention(const replay_kv_layer* layer, const replay_kv_
     const long long cap = (long long)x.max_pages * layer->page_size, seen = (long long)a.window + x.ntok - 1 + 31;
     // (short ranges are over sooner than their order is found: 2048 of 200 tokens 47 us as they stand, 58 by length)
     const long long most = a.window > 0 && seen < cap ? seen : cap, ranges = (long long)x.batch * Hkv * p.nchunk;
-    a.whole = rs::kv_attention_whole(most, ranges);
-    a.by_length = most > 1280 && ranges > p.nwg && ranges < (1 << 22) && x.batch <= rs::KV_BY_LENGTH;
+    a.whole = rs::kv_attention_whole(p, D, fp8, most, ranges);
+    a.by_length = (most > 1280 || !a.whole) && ranges > p.nwg && ranges < (1 << 22) && x.batch <= rs::KV_BY_LENGTH;
     a.nwg = p.nwg;
     a.scale_log2 = (float)((double)x.scale * 1.4426950408889634);
-    const bool bf = layer->io_dtype == REPLAY_BF16, fp8 = layer->cache_dtype == REPLAY_FP8_E4M3;
+    const bool bf = layer->io_dtype == REPLAY_BF16;
     const auto run = bf ? (fp8 ? rs::launch_kv_attention_bf16_fp8 : rs::launch_kv_attention_bf16)
                         : (fp8 ? rs::launch_kv_attention_f16_fp8 : rs::launch_kv_attention_f16);
     return LAUNCH(run(a, p, D, (hipStream_t)stream), "paged attention");

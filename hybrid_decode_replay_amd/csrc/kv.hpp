@@ -80,7 +80,7 @@ constexpr int kv_occ(int D, bool fp8, int RB)
 KvPlan kv_attention_plan(int D, bool fp8, int rows);
 constexpr int KV_BY_LENGTH = 1024;       // sequences that can be taken in the order of their lengths
 // Whether ranges of at most `tokens` tokens are short enough for a workgroup each.
-bool kv_attention_whole(long long tokens, long long ranges);
+bool kv_attention_whole(const KvPlan& p, int D, bool fp8, long long tokens, long long ranges);
 // One translation unit per io and cache type.
 hipError_t launch_kv_attention_bf16(const KvAttention& a, const KvPlan& p, int D, hipStream_t s);
 hipError_t launch_kv_attention_bf16_fp8(const KvAttention& a, const KvPlan& p, int D, hipStream_t s);
