@@ -554,7 +554,8 @@ size_t replay_kv_attention_workspace(const replay_kv_layer *layer, int32_t batch
  * A token that sees nothing (p < 0, or only positions without a page) gives
  * o = 0 and lse = -inf.  What lies in masked positions does not matter, NaN
  * included.  Softmax statistics and sums are fp32; weights are carried in two
- * io_dtype terms. */
+ * io_dtype terms (so an infinite value leaves NaN, not an infinity, in its
+ * channel of the tokens that see it). */
 replay_status replay_kv_attention(const replay_kv_layer *layer, const replay_kv_attention_args *args, void *ws,
                                   size_t ws_bytes, void *stream);
 
