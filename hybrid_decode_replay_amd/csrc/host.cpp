@@ -18,7 +18,8 @@ namespace rs {
 // Rows that share a key/value head fill 16-row products.  Up to 32 rows a wave takes one or two such
 // blocks and the waves of a workgroup split the tokens; past that the cache goes through LDS and the
 // waves take different rows.  Wide heads have one block a wave there (registers).  More rows than a
-// workgroup holds make further chunks, which read the cache again.
+// workgroup holds make further chunks, which read the cache again (128 channels, 128 rows 155 us, 256 rows in
+// two chunks 264).
 KvPlan kv_attention_plan(int D, bool fp8, int rows)
 {
     KvPlan p;

@@ -70,9 +70,10 @@ struct KvPlan {
     bool wide;
     int rpc, nchunk, nwg;
 };
-// Workgroups of four waves per CU: two, or one where two would not leave a wave the registers for
-// its outputs and the blocks on their way (a spilled token loop runs at half the rate: 64 queries on
-// 256 channels 510 us with two, 186 us with one; three for the narrow ones gain nothing).
+// Workgroups of four waves per CU where keys and values go straight to registers: two, or one where two
+// would not leave a wave the registers for its outputs and the blocks on their way.  A token loop that
+// spills is slower (537 MB of bf16 cache, one workgroup against two: 256 channels, 4 rows 96 / 125 us, 32
+// rows 109 / 230; 128 channels, 32 rows 94 / 116); three for the narrow ones gain nothing.
 constexpr int kv_occ(int D, bool fp8, int RB)
 {
     return D == 256 || (D == 128 && RB == 2 && !fp8) ? 1 : 2;

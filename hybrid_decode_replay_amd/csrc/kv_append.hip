@@ -7,11 +7,15 @@
 // lanes write neighbouring chunks (32-byte pieces per lane cost streamed stores 40 %).  The row's
 // cosines and sines are formed once, in LDS, and serve all of its heads: the angle is pos * freq in
 // fp64 as a fraction of a turn (exact to 2^-52 of the number of turns, so a position of 10^6 still has
-// its angle to 10^-9), the fraction goes to sincospi in fp32.
+// its angle to 10^-9), the fraction goes to sincospi in fp32 (off by at most 2^-26 of a turn, 1e-7
+// radians, of the order of sine's and cosine's own fp32 roundings).
 //
 // Bound by HBM: q, k and v are read once and written once.  16387 rows of 32 + 2 x 8 heads of 128
-// channels, 403 MB: 73 us, 5.5 TB/s, against 5.9 TB/s of a copy.  1024 rows on an E4M3 cache 6.2 us, one
-// row 2.8 (launch and three dependent loads).
+// channels, 403 MB: 73 us, 5.5 TB/s, against 5.9 TB/s of a copy; on an E4M3 cache, 369 MB, 69 us.  1024 rows
+// of 16 + 2 x 2 heads of 256 on an E4M3 cache 6.2 us, one row 2.9 (launch and three dependent loads).  Rows
+// of more items than one pass holds wait for their next pass's loads: 64 + 2 x 8 heads of 128, 671 MB, 120
+// us (5.6 TB/s), of 256 channels 255 us (5.3), 1024 such rows 11.5 and 17.4 us.  Idle rows are read (the loads
+// do not wait for the slots): with a quarter of 16387 idle 107 us for 120.
 #include <type_traits>
 
 #include "kv_io.hpp"

@@ -32,13 +32,17 @@
 //    alone, so results repeat.  Ranges known to be short (kv_attention_whole) and many ranges of like
 //    lengths (kv_order) get a workgroup each instead.
 //  * Weights are carried as two io-type terms (hi + lo, relative 2^-16 for bf16, 2^-22 for fp16): one
-//    term alone would double the error of the output's own rounding, and the products have room.
+//    term alone would double the error of the output's own rounding.  A third bf16 term (24 bits) moves
+//    one output in 600 by a step and leaves the error against 64 bits at the rounding's own 0.0017; it
+//    costs 1 % up to 32 rows, and 18 % with 128 rows on 128 channels (151 -> 178 us).
 //  * More than 32 rows of a head (drafts x queries) would make the waves of a workgroup read the cache
 //    again for each other: there it goes through LDS (kv_attention_wide_kernel).
 //
 // Measured with both launches, 537 MB of cache (131k tokens of 8 heads, 128 channels, bf16), read alone
-// in 77 us at the 7.0 TB/s of a plain read: 92 us for 4 rows a head, 94 for 32, 107 for 64, 150 for 128.
-// The same bytes as E4M3 take 97 us, on 64 channels 95, on 256 channels 95 (4 rows a head).
+// in 76 us at the 7.09 TB/s of a plain read: 93 us for 4 rows a head, 94 for 32, 107 for 64, 155 for 128, 264
+// for 256 (two chunks).  The same bytes on 64 channels 93 (64 rows 117), on 256 channels 96 (32 rows 109, 64
+// rows 122, 128 rows in two chunks 204), as E4M3 97 (32 rows 110, 64 rows 157, 128 rows 260: twice the tokens,
+// and past 32 rows the work on a token counts, not its bytes).
 #pragma once
 #include <type_traits>
 

@@ -9,8 +9,8 @@
 // What bounds them: nothing but latency.  A step moves some kilobytes; one workgroup loads len,
 // held and the mask together, scans, and writes (a few dependent trips to L2).  Only packed rows
 // and releases, which can move a megabyte of entries, take a second launch over many workgroups.
-// Measured: reserve 2.8 us for 8 sequences, 3.8 for 4 drafts of 512; commit 1.6 and 2.0; packed rows of
-// 128 prompts of up to 8011 tokens 4.4 + 5.2; release of 128 such sequences 2.4 + 3.2.
+// Measured: reserve 2.3 us for 8 sequences, 4.2 for 4 drafts of 512; commit 1.3 and 2.2; packed rows of
+// 128 prompts of up to 8011 tokens 4.5 + 5.3; release of 128 such sequences 2.4 + 3.1.
 #include "common.hpp"
 #include "kv.hpp"
 
