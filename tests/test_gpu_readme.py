@@ -17,7 +17,10 @@ def _gpu():
 
 
 def example():
-    with open(os.path.join(ROOT, "README.md")) as f:
+    path = os.path.join(ROOT, "README.md")
+    if not os.path.exists(path):
+        pytest.skip("a copy without its README")
+    with open(path) as f:
         blocks = f.read().split("```")[1::2]
     found = [b for b in blocks if "rb.KVPages" in b]
     assert len(found) == 1
