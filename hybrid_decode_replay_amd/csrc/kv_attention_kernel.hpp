@@ -34,7 +34,8 @@
 //  * Weights are carried as two io-type terms (hi + lo, relative 2^-16 for bf16, 2^-22 for fp16): one
 //    term alone would double the error of the output's own rounding.  A third bf16 term (24 bits) moves
 //    one output in 600 by a step and leaves the error against 64 bits at the rounding's own 0.0017; it
-//    costs 1 % up to 32 rows, and 18 % with 128 rows on 128 channels (151 -> 178 us).
+//    costs 1 % for 4 rows of a head, 1 to 5 % for 32, 6 % for 64 and 18 % for 128 on 128 channels (151 ->
+//    178 us).
 //  * More than 32 rows of a head (drafts x queries) would make the waves of a workgroup read the cache
 //    again for each other: there it goes through LDS (kv_attention_wide_kernel).
 //
