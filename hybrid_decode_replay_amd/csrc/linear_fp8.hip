@@ -8,10 +8,13 @@
 //
 //   E4M3   one v_mfma_f32_16x16x128_f8f6f4.  The unit adds eight products at a time, each cut (towards zero) 13 binary
 //          places below the largest of the eight, and such sums in fp32.  What is lost is some 2^-16 of the sum of
-//          magnitudes, an eighth of a bf16 rounding where nothing cancels: the way of bf16 outputs.
+//          magnitudes, an eighth of a bf16 rounding where nothing cancels: the way of bf16 outputs of more than 64 rows.
 //   exact  codes turned into bf16 (which holds every E4M3 number) and four v_mfma_f32_16x16x32_bf16, whose sums are fp32.
 //          Half the rate (2.2 against 4.4 PFLOP/s in a loop of nothing else) and the conversions.  The way of fp16
-//          outputs, whose rounding is as fine as the cut (2.1e-4 of the result by rounding alone, 3.5e-4 with the cut).
+//          outputs, whose rounding is as fine as the cut (2.1e-4 of the result by rounding alone, 3.5e-4 with the cut), and
+//          of up to 64 rows of either type, which the weights' bytes bound (rows by 4096 and 16448 outputs of 4096 channels,
+//          weights from HBM, us, exact and cut: 1 row 7.1 and 5.9, 18.8 and 18.4; 32 rows 8.4 and 6.9, 24.8 and 23.8; 64 rows
+//          10.9 and 8.2, 27.5 and 25.2).
 #include "kv_io.hpp"
 #include "mixer.hpp"
 
@@ -320,10 +323,10 @@ __global__ void __launch_bounds__(64 * WM * WN * WK, OCC) linear_tile_kernel(Lin
 
 namespace {
 
-template <int IO, int BM, int BN, int WM, int WN, int KB, int ST, int WK = 1, int OCC = 2>
+template <int IO, bool EXACT, int BM, int BN, int WM, int WN, int KB, int ST, int WK = 1, int OCC = 2>
 hipError_t run_tile(const LinearArgs& a, hipStream_t s)
 {
-    linear_tile_kernel<IO, IO == KV_F16, BM, BN, WM, WN, KB, ST, WK, OCC>
+    linear_tile_kernel<IO, EXACT, BM, BN, WM, WN, KB, ST, WK, OCC>
         <<<(uint32_t)((a.m + BM - 1) / BM) * (uint32_t)((a.n + BN - 1) / BN), 64 * WM * WN * WK, 0, s>>>(a);
     return hipGetLastError();
 }
@@ -351,60 +354,65 @@ int cheapest(const LinearArgs& a, const TileCost (&shapes)[N])
     return best;
 }
 
-// Up to 32 rows there is one tile row, and the workgroups are what the outputs make of them.  Up to one of 32 outputs for each
-// CU, four blocks a step by four teams of waves (us at 4096 channels; 16 rows by 4096 outputs 5.7, by 8192 7.5; 32 rows 6.4 and
-// 7.6), else teams of four blocks each (7.3, 8.1, by 12288 9.7 against 9.8, by 16448 12.5 against 14.6: 5.4 TB/s; 32 rows 8.0,
-// 8.8, by 12288 10.5 against 12.6), and of more than two for each CU 64 outputs (32 rows by 12288 11.1, by 16448 15.5 against
-// 17.4).
-// More rows take the cheapest shape.  Measured, rows x outputs (64 x 32 four teams, 64 x 64 two teams, 64 x 64, 64 x 128, 64 x
-// 144, 128 x 128 two teams, 128 x 128, 128 x 144, 256 x 128, 256 x 256): 64 x 8192 8.9, 11.1, 11; 256 x 4096 17, 11.4, 13.4,
+// Up to 64 rows, exact.  Up to 32 there is one tile row, and the workgroups are what the outputs make of them: four blocks a
+// step by four teams of waves (us at 4096 channels; 16 rows by 4096 outputs 6.7, two stages instead of three 7.1, by 8192 8.0
+// both, by 12288 10.7 and 9.9, by 32768 33.5 and 33.0; 32 rows in 32 outputs or 64: by 4096 8.0 and 10.3, by 12288 11.2 and
+// 11.7, by 16448 17.6 and 17.4).  More take the cheapest shape (128 rows by 4096 outputs in 64 x 32 by four teams and 64 x 64
+// by four 10.8 and 14.6).
+template <int IO>
+hipError_t pick_few(const LinearArgs& a, hipStream_t s)
+{
+    if (a.m <= 16) return a.n <= 256 * 32 ? run_tile<IO, true, 16, 32, 1, 2, 1, 3, 4>(a, s) : run_tile<IO, true, 16, 32, 1, 2, 1, 2, 4>(a, s);
+    if (a.m <= 32) return run_tile<IO, true, 32, 32, 2, 1, 1, 2, 4>(a, s);
+    static const TileCost shapes[] = {{64, 32, 10.8f, 0}, {64, 64, 15.4f, 0}, {64, 128, 22.8f, 0}, {64, 144, 25.7f, 0}};
+    switch (cheapest(a, shapes)) {
+    case 0: return run_tile<IO, true, 64, 32, 4, 1, 1, 2, 4>(a, s);
+    case 1: return run_tile<IO, true, 64, 64, 2, 2, 1, 2, 4>(a, s);
+    case 2: return run_tile<IO, true, 64, 128, 2, 2, 1, 2, 2>(a, s);
+    default: return run_tile<IO, true, 64, 144, 2, 3, 1, 2, 2, 3>(a, s);
+    }
+}
+
+// More rows, bf16: the cheapest shape.  Measured, rows x outputs (64 x 32 four teams, 64 x 64 two teams, 64 x 64, 64 x 128, 64 x
+// 144, 128 x 128 two teams, 128 x 128, 128 x 144, 256 x 128, 256 x 256): 256 x 4096 17, 11.4, 13.4,
 // 17.2, 18, 21.3, 24.7; 128 x 16448 -, 30.8, 27.7, 21.3, 19.3, 22.4, 26.2, 23.6; 256 x 16448 -, 49, 44, 41, 36.8, 43, 35.4, 26.5;
 // 1024 x 4096 54, 44, 32, 25.1, 35.5, 23.7, 26.9, 25.1, 33, 50; 2048 x 4096 104, 81, 59, 46, 68, 44, 38.8, 47, 37.4, 52;
 // 2048 x 8192 209, 156, 116, 89, 137, 88, 74, 94, 72, 61.5.
 hipError_t pick_bf16(const LinearArgs& a, hipStream_t s)
 {
     constexpr int IO = KV_BF16;
-    if (a.m <= 16) return a.n <= 256 * 32 ? run_tile<IO, 16, 32, 1, 2, 1, 3, 4>(a, s) : run_tile<IO, 16, 32, 1, 2, 4, 2>(a, s);
-    if (a.m <= 32) {
-        if (a.n <= 256 * 32) return run_tile<IO, 32, 32, 1, 2, 1, 3, 4>(a, s);
-        return a.n <= 512 * 32 ? run_tile<IO, 32, 32, 2, 2, 4, 2>(a, s) : run_tile<IO, 32, 64, 2, 2, 2, 3>(a, s);
-    }
     static const TileCost shapes[] = {{64, 32, 8.6f, 0}, {64, 64, 11.3f, 0}, {64, 64, 12.6f, 17.2f}, {64, 128, 17.3f, 26.6f},
                                       {64, 144, 18.7f, 0}, {128, 128, 23.5f, 0}, {128, 128, 25.f, 38.f}, {128, 144, 25.5f, 0},
                                       {256, 128, 35.f, 0}, {256, 256, 54.f, 0}};
     switch (cheapest(a, shapes)) {
-    case 0: return run_tile<IO, 64, 32, 4, 1, 1, 3, 4>(a, s);
-    case 1: return run_tile<IO, 64, 64, 2, 2, 1, 3, 2>(a, s);
-    case 2: return run_tile<IO, 64, 64, 2, 2, 2, 2>(a, s);
-    case 3: return run_tile<IO, 64, 128, 2, 2, 1, 3>(a, s);
-    case 4: return run_tile<IO, 64, 144, 2, 3, 1, 2, 2, 3>(a, s);
-    case 5: return run_tile<IO, 128, 128, 2, 2, 1, 2, 2>(a, s);
-    case 6: return run_tile<IO, 128, 128, 2, 2, 1, 2>(a, s);
-    case 7: return run_tile<IO, 128, 144, 2, 3, 1, 2, 2, 3>(a, s);
-    case 8: return run_tile<IO, 256, 128, 4, 2, 1, 3>(a, s);
-    default: return run_tile<IO, 256, 256, 4, 2, 1, 2>(a, s);
+    case 0: return run_tile<IO, false, 64, 32, 4, 1, 1, 3, 4>(a, s);
+    case 1: return run_tile<IO, false, 64, 64, 2, 2, 1, 3, 2>(a, s);
+    case 2: return run_tile<IO, false, 64, 64, 2, 2, 2, 2>(a, s);
+    case 3: return run_tile<IO, false, 64, 128, 2, 2, 1, 3>(a, s);
+    case 4: return run_tile<IO, false, 64, 144, 2, 3, 1, 2, 2, 3>(a, s);
+    case 5: return run_tile<IO, false, 128, 128, 2, 2, 1, 2, 2>(a, s);
+    case 6: return run_tile<IO, false, 128, 128, 2, 2, 1, 2>(a, s);
+    case 7: return run_tile<IO, false, 128, 144, 2, 3, 1, 2, 2, 3>(a, s);
+    case 8: return run_tile<IO, false, 256, 128, 4, 2, 1, 3>(a, s);
+    default: return run_tile<IO, false, 256, 256, 4, 2, 1, 2>(a, s);
     }
 }
 
-// The same for exact products (the conversions weigh more, a tile of 256 x 256 would not fit the registers).  16 rows by 4096
-// outputs 6.7 us, two stages instead of three 7.1, by 8192 8.0 both, by 12288 10.7 and 9.9, by 32768 33.5 and 33.0.  32 rows in
-// 32 outputs or 64: by 4096 8.0 and 10.3, by 12288 11.2 and 11.7, by 16448 17.6 and 17.4.  More (64 x 32 four teams, 64 x 64
-// four teams, 64 x 128, 64 x 144, 128 x 128, 128 x 256): 128 x 4096 10.8, 14.6; 256 x 4096 22, 16.5, 23.5, 26.3, 34; 512 x 4096
+// The same for exact products (the conversions weigh more, a tile of 256 x 256 would not fit the registers; 64 x 32 four teams,
+// 64 x 64 four teams, 64 x 128, 64 x 144, 128 x 128, 128 x 256): 256 x 4096 22, 16.5, 23.5, 26.3, 34; 512 x 4096
 // 39, 29, 23.7; 256 x 16448 91, 71, 68, 52, 69, 59; 512 x 8192 76, 54, 45, 50, 36, 58; 1024 x 8192 151, 105, 87, 97, 69, 64.
 hipError_t pick_f16(const LinearArgs& a, hipStream_t s)
 {
     constexpr int IO = KV_F16;
-    if (a.m <= 16) return a.n <= 256 * 32 ? run_tile<IO, 16, 32, 1, 2, 1, 3, 4>(a, s) : run_tile<IO, 16, 32, 1, 2, 1, 2, 4>(a, s);
-    if (a.m <= 32) return run_tile<IO, 32, 32, 2, 1, 1, 2, 4>(a, s);
     static const TileCost shapes[] = {{64, 32, 10.8f, 0}, {64, 64, 15.4f, 0}, {64, 128, 22.8f, 0}, {64, 144, 25.7f, 0},
                                       {128, 128, 34.f, 0}, {128, 256, 58.f, 0}};
     switch (cheapest(a, shapes)) {
-    case 0: return run_tile<IO, 64, 32, 4, 1, 1, 2, 4>(a, s);
-    case 1: return run_tile<IO, 64, 64, 2, 2, 1, 2, 4>(a, s);
-    case 2: return run_tile<IO, 64, 128, 2, 2, 1, 2, 2>(a, s);
-    case 3: return run_tile<IO, 64, 144, 2, 3, 1, 2, 2, 3>(a, s);
-    case 4: return run_tile<IO, 128, 128, 2, 2, 1, 2, 2>(a, s);
-    default: return run_tile<IO, 128, 256, 2, 4, 1, 3>(a, s);
+    case 0: return run_tile<IO, true, 64, 32, 4, 1, 1, 2, 4>(a, s);
+    case 1: return run_tile<IO, true, 64, 64, 2, 2, 1, 2, 4>(a, s);
+    case 2: return run_tile<IO, true, 64, 128, 2, 2, 1, 2, 2>(a, s);
+    case 3: return run_tile<IO, true, 64, 144, 2, 3, 1, 2, 2, 3>(a, s);
+    case 4: return run_tile<IO, true, 128, 128, 2, 2, 1, 2, 2>(a, s);
+    default: return run_tile<IO, true, 128, 256, 2, 4, 1, 3>(a, s);
     }
 }
 
@@ -412,6 +420,7 @@ hipError_t pick_f16(const LinearArgs& a, hipStream_t s)
 
 hipError_t launch_linear_fp8(const LinearArgs& a, int io, hipStream_t s)
 {
+    if (a.m <= 64) return io == MIX_BF16 ? pick_few<KV_BF16>(a, s) : pick_few<KV_F16>(a, s);
     return io == MIX_BF16 ? pick_bf16(a, s) : pick_f16(a, s);
 }
 
