@@ -76,21 +76,6 @@ __device__ __forceinline__ void to_lds(const void* from, void* to)
     else __builtin_amdgcn_global_load_lds(f, t, 4, 0, 0);
 }
 
-// Four consecutive outputs j .. j + 3 of one row.
-template <int IO>
-__device__ __forceinline__ void store4(uint16_t* row, int j, int n, bool wide, f32x4 v)
-{
-    const u32x2 w = {kv_pack<IO>(v.x, v.y), kv_pack<IO>(v.z, v.w)};
-    if (wide && j + 4 <= n) {
-        *reinterpret_cast<u32x2*>(row + j) = w;
-    } else {
-        if (j < n) row[j] = (uint16_t)w.x;
-        if (j + 1 < n) row[j + 1] = (uint16_t)(w.x >> 16);
-        if (j + 2 < n) row[j + 2] = (uint16_t)w.y;
-        if (j + 3 < n) row[j + 3] = (uint16_t)(w.y >> 16);
-    }
-}
-
 // A workgroup of WM x WN waves, or WK times as many, takes BM rows by BN outputs.  Blocks of channels of both operands are
 // brought straight to LDS, ST - 1 steps of WK KB blocks on their way while one is multiplied; rows of 128 bytes, their
 // 16-byte chunks exchanged by the row's low three bits, so that the 16 rows of an operand read are spread over the banks.
