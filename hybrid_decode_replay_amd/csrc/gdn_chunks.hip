@@ -380,6 +380,7 @@ __device__ __forceinline__ bool state_of(const PrefillArgs& a, const uint8_t* ws
             S[n][i] = a.S_in ? ld4(a.S_in + sat + (size_t)(col[n] + r) * R + 32 * (t >> 1) + 4 * (t & 1)) : f32x4{0.f, 0.f, 0.f, 0.f};
         }
     if (nc > 0) tell_state();
+    float none = 0.f;                                       // NaN once an o was an infinity or NaN
     // One chunk; BOTH: it has more than 32 tokens.  (Of fewer, waves 2 and 3 have none, and U has none behind them.)
     auto chunk = [&](auto BOTH, int c) {
         constexpr bool both = decltype(BOTH)::value;
@@ -519,6 +520,10 @@ __device__ __forceinline__ bool state_of(const PrefillArgs& a, const uint8_t* ws
 #pragma unroll
             for (int n = 0; n < NS; ++n)
 #pragma unroll
+                for (int i = 0; i < 4; ++i) none = __builtin_fmaf(o[n][i], 0.f, none);
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
                 for (int i = 0; i < 4; ++i) turn[w][n][(4 * q + i) * 16 + r] = f32_to_bf16_bits(o[n][i]);
             wave_lds_sync();
             const int row = tile_row(w, lane >> 2), left = s.count - c * CHUNK;
@@ -534,7 +539,7 @@ __device__ __forceinline__ bool state_of(const PrefillArgs& a, const uint8_t* ws
     if (nc > 0) {
         if (tail > 32) chunk(std::true_type{}, nc - 1);
         else chunk(std::false_type{}, nc - 1);
-        int bad = 0;
+        int bad = !(none == 0.f);
 #pragma unroll
         for (int n = 0; n < NS; ++n)
 #pragma unroll

@@ -255,6 +255,10 @@ __global__ void __launch_bounds__(256, R == 256 ? 1 : 2) gdn_short_kernel(Prefil
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) bad |= not_finite(S[t][e]);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) bad |= not_finite(o[t][e]);
         if (__ballot(bad)) {
             again |= 1u << strip;
             continue;

@@ -262,3 +262,19 @@ def test_what_a_token_must_not_see(rb, DK, DV, n, what, value):
             assert good[rest].all() and fine.all() and not o[j, 1].isfinite().any()
         else:
             assert good[:j].all() and not o[j:n, 1].isfinite().any() and not S[0, 1].isfinite().all(-1).any()
+
+
+@pytest.mark.parametrize("DK", [64, 128, 256])
+@pytest.mark.parametrize("lens,H,DV", [([20], 2, 32), ([32], 1, 96), ([70], 2, 32), ([100, 30], 2, 48), ([66] * 4 + [0], 32, 80),
+                                       ([40] + [9] * 39, 32, 48)])
+def test_scores_that_overflow(rb, DK, lens, H, DV):
+    """q and k whose products pass the fp32 range, over updates so small that every output and state is an ordinary number:
+    short sequences alone, chunks with one and two strips a workgroup, long sequences among short ones."""
+    rows = sum(lens)
+    q, k, v, a, b = gdn_inputs(17, rows, H, 1, DK, DV, BF)
+    q, k = (q.float() * 2.0 ** 100).to(BF), (k.float() * 2.0 ** 32).to(BF)
+    v, b = (v.float() * 2.0 ** -34).to(BF), b * 2.0 ** -64
+    starts = starts_of(lens)
+    o, S = rb.gdn_prefill(*(t.cuda() for t in (q, k, v, a, b)), starts.cuda(), ngroups=1)
+    assert o.isfinite().all() and S.isfinite().all()
+    check(o, S, q, k, v, a, b, starts, 1, 1.0, None)
