@@ -7,6 +7,7 @@
 namespace rs {
 
 typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int CHUNK = GDN_CHUNK;
 static_assert(CHUNK == 64, "tiles and fragments are laid out for 64 tokens");
@@ -135,6 +136,31 @@ __device__ __forceinline__ double prefix_sum(double x)
     x += lanes_before<0x142, 0xa>(x);              // a row's last lane to the next row (of 1 and 3),
     return x + lanes_before<0x143, 0xc>(x);        // lane 31 to the rows behind it
 }
+
+// The g's of a chunk (products of alpha over its tokens up to each) as powers of two, 2^(whole + part): sums of log2 alpha in
+// 64 bits, whose whole part is kept apart, so that the ratio of two g's is as near for far tokens as for near ones.  The
+// logarithm is alpha's exponent and the fp32 logarithm of a mantissa in [1/sqrt 2, sqrt 2): off by some 2^-25 a token whatever
+// alpha is, as a product of the alphas in fp32 would be.  alpha 0 counts as 2^-200 (no fp32 number is left after it); tokens
+// that are not live keep the state.
+struct Power {
+    int whole;
+    float part;
+};
+__device__ __forceinline__ Power decay_of(float alpha, bool live)
+{
+    float m = __builtin_amdgcn_frexp_mantf(alpha);
+    int e = __builtin_amdgcn_frexp_expf(alpha);
+    if (m < 0.70710678f) {
+        m += m;
+        --e;
+    }
+    const double l = (double)log2f(m) + (double)e;
+    const double x = prefix_sum(!live ? 0.0 : l < -200.0 ? -200.0 : l);
+    const double w = floor(fmax(fmin(x, 16384.0), -16384.0));      // (of an infinity or NaN: the part is one)
+    return Power{(int)w, (float)(x - w)};
+}
+// 2^(whole + part), parts being differences of two: within 1 of 0.
+__device__ __forceinline__ float power(int whole, float part) { return __builtin_ldexpf(__builtin_amdgcn_exp2f(part), whole); }
 
 // 0, or 1 where x is an infinity or NaN.
 __device__ __forceinline__ int not_finite(float x) { return (__builtin_bit_cast(uint32_t, x) & 0x7f800000u) == 0x7f800000u; }

@@ -35,7 +35,8 @@ __global__ void __launch_bounds__(256, R == 256 ? 1 : 4) gdn_chunk_kernel(Prefil
     constexpr int M = R / 32, RB = R * 2, CPR = RB / 16, KL = CPR / 4;
     constexpr int MAT = CHUNK * LD * 4, ROWS = 2 * CHUNK * RB;
     __shared__ __attribute__((aligned(16))) uint8_t both[ROWS > 2 * MAT ? ROWS : 2 * MAT];    // k and q, then T and A
-    __shared__ __attribute__((aligned(16))) float ghi[CHUNK], glo[CHUNK], bt[CHUNK];
+    __shared__ __attribute__((aligned(16))) int gw[CHUNK];
+    __shared__ __attribute__((aligned(16))) float gp[CHUNK], bt[CHUNK];
     float *tm = reinterpret_cast<float*>(both), *am = reinterpret_cast<float*>(both + MAT);
     // 16-byte chunks of a row are exchanged by this, so that 16 rows in order, and in a tile's order, are spread over the banks
     auto key = [](int row) { return ((row & 3) | (row >> 1 & 4) | (((row << 1) ^ (row >> 1)) & 8)) & (CPR - 1); };
@@ -59,8 +60,7 @@ __global__ void __launch_bounds__(256, R == 256 ? 1 : 4) gdn_chunk_kernel(Prefil
     const Span s = span_of(a, b);
     const int first = s.first + (slot - uni(at_slot)) * CHUNK, n = min(CHUNK, s.first + s.count - first);
 
-    // log2 of a head's g's: sums of log2 alpha in 64 bits, as two fp32 terms; alpha 0 as 2^-200 (no fp32 number is left after
-    // it); tokens behind the last keep the state (and their beta is 0)
+    // (tokens behind the last keep the state, and their beta is 0)
     float al, be;
     auto ask_gates = [&](int h) {
         const size_t at = (size_t)(first + min(lane, n - 1)) * a.H + h;
@@ -69,11 +69,9 @@ __global__ void __launch_bounds__(256, R == 256 ? 1 : 4) gdn_chunk_kernel(Prefil
     };
     auto gates = [&]() {
         const bool live = lane < n;
-        const float l = log2f(al);
-        const double x = prefix_sum(!live ? 0.0 : l < -200.f ? -200.0 : (double)l);
-        const float hi = (float)x;
-        ghi[lane] = hi;
-        glo[lane] = (float)(x - (double)hi);
+        const Power g2 = decay_of(al, live);
+        gw[lane] = g2.whole;
+        gp[lane] = g2.part;
         bt[lane] = live ? be : 0.f;
     };
     // (rows behind the last token repeat it)
@@ -144,15 +142,17 @@ __global__ void __launch_bounds__(256, R == 256 ? 1 : 4) gdn_chunk_kernel(Prefil
     for (int h = grp * a.hpg; h < (grp + 1) * a.hpg; ++h) {
         uint8_t* out = ws + ((size_t)slot * a.H + h) * GDN_CHUNK_BYTES;
         // (of places that are masked, whose products are 0, a finite number)
-        auto since = [&](float hi, float lo, float hj, float lj) { return __builtin_amdgcn_exp2f(fminf((hi - hj) + (lo - lj), 126.f)); };
+        auto since = [&](int wi, float pi, int wj, float pj) { return power(min(wi - wj, 126), pi - pj); };
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (!has(i)) continue;
             const int col = 16 * cols[i] + r, row = 16 * rows[i] + 4 * q;
-            const f32x4 hi = ld4(ghi + row), lo = ld4(glo + row), be4 = ld4(bt + row);
-            const float hj = ghi[col], lj = glo[col];
+            const i32x4 wi = *reinterpret_cast<const i32x4*>(gw + row);
+            const f32x4 pi = ld4(gp + row), be4 = ld4(bt + row);
+            const int wj = gw[col];
+            const float pj = gp[col];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) am[(row + e) * LD + col] = be4[e] * since(hi[e], lo[e], hj, lj) * kk[i][e];
+            for (int e = 0; e < 4; ++e) am[(row + e) * LD + col] = be4[e] * since(wi[e], pi[e], wj, pj) * kk[i][e];
         }
         __syncthreads();
         if (w == 0) {
@@ -175,23 +175,24 @@ __global__ void __launch_bounds__(256, R == 256 ? 1 : 4) gdn_chunk_kernel(Prefil
                 if (!has_p) break;
                 int t, sg;
                 const int f = piece(e, t, sg), i = tile_row(t, r), j0 = 32 * sg + 8 * q;
-                const float hi = ghi[i], lo = glo[i];
+                const int wi = gw[i];
+                const float pi = gp[i];
                 f32x4 p[2];
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        p[x][k] = since(hi, lo, ghi[j0 + 4 * x + k], glo[j0 + 4 * x + k]) * kq[e][x][k];
+                        p[x][k] = since(wi, pi, gw[j0 + 4 * x + k], gp[j0 + 4 * x + k]) * kq[e][x][k];
                 const Terms3 c = cut3(p[0], p[1]);
                 *reinterpret_cast<bf16x8*>(out + (PIECE_P + f) * 1024 + lane * 16) = c.t[0];
                 *reinterpret_cast<bf16x8*>(out + (PIECE_P + FRAGS + f) * 1024 + lane * 16) = c.t[1];
             }
             if (w == 1) {
                 float* g = reinterpret_cast<float*>(out + PIECE_G * 1024);
-                const float hi = ghi[lane], lo = glo[lane], whole = __builtin_amdgcn_exp2f(hi + lo);
+                const float whole = power(gw[lane], gp[lane]);
                 g[lane] = whole;
                 g[CHUNK + lane] = a.scale * whole;
-                g[2 * CHUNK + lane] = since(ghi[CHUNK - 1], glo[CHUNK - 1], hi, lo);
+                g[2 * CHUNK + lane] = power(gw[CHUNK - 1] - gw[lane], gp[CHUNK - 1] - gp[lane]);
             }
         }
         __syncthreads();

@@ -16,7 +16,8 @@ __global__ void __launch_bounds__(256, R == 256 ? 1 : 2) gdn_short_kernel(Prefil
     __shared__ __attribute__((aligned(16))) uint8_t kbuf[N * RB], qbuf[N * RB];
     __shared__ __attribute__((aligned(16))) float am[N * LD], tm[N * LD], pm[N * LD];
     __shared__ __attribute__((aligned(16))) uint16_t turn[4][2][16 * 16];      // v, then o, of a wave's strip
-    __shared__ float ghi[N], glo[N], bt[N];
+    __shared__ int gw[N];
+    __shared__ float gp[N], bt[N];
     const int tid = threadIdx.x, lane = tid & 63, w = uni(tid >> 6), r = lane & 15, q = lane >> 4;
     const int bh = blockIdx.x, b = bh / a.H, h = bh - b * a.H, g = h / a.hpg;
     const Span s = span_of(a, b);
@@ -80,19 +81,16 @@ __global__ void __launch_bounds__(256, R == 256 ? 1 : 2) gdn_short_kernel(Prefil
         }
     }
     if (w == 3) {
-        // log2 of the g's: sums of log2 alpha in 64 bits, as two fp32 terms; alpha 0 as 2^-200; tokens behind the last keep the state
         const bool live = lane < n;
-        const float l = log2f(al);
-        const double x = prefix_sum(!live ? 0.0 : l < -200.f ? -200.0 : (double)l);
+        const Power g2 = decay_of(al, live);
         if (lane < N) {
-            const float hi = (float)x;
-            ghi[lane] = hi;
-            glo[lane] = (float)(x - (double)hi);
+            gw[lane] = g2.whole;
+            gp[lane] = g2.part;
             bt[lane] = live ? be : 0.f;
         }
     }
     lds_barrier();
-    auto since = [&](float hi, float lo, int j) { return __builtin_amdgcn_exp2f((hi - ghi[j]) + (lo - glo[j])); };
+    auto since = [&](int i, int j) { return power(gw[i] - gw[j], gp[i] - gp[j]); };
     if (w < 3) {
         // tiles (0, 0), (1, 1) and (1, 0) of K K^T and Q K^T, rows and columns in order
         const int rt = w > 0 ? 1 : 0, ct = w == 1 ? 1 : 0;
@@ -111,7 +109,7 @@ __global__ void __launch_bounds__(256, R == 256 ? 1 : 2) gdn_short_kernel(Prefil
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int row = 16 * rt + 4 * q + e;
-            const float d = since(ghi[row], glo[row], col);
+            const float d = since(row, col);
             am[row * LD + col] = col < row ? bt[row] * d * kk[e] : 0.f;
             pm[row * LD + col] = col <= row ? a.scale * d * qk[e] : 0.f;
         }
@@ -199,11 +197,11 @@ __global__ void __launch_bounds__(256, R == 256 ? 1 : 2) gdn_short_kernel(Prefil
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int row = tile_row(t, 4 * q + e);
-            gi[t][e] = __builtin_amdgcn_exp2f(ghi[row] + glo[row]);
-            gd[t][e] = since(ghi[N - 1], glo[N - 1], row);
+            gi[t][e] = power(gw[row], gp[row]);
+            gd[t][e] = since(N - 1, row);
         }
     }
-    const float whole = __builtin_amdgcn_exp2f(ghi[N - 1] + glo[N - 1]);
+    const float whole = power(gw[N - 1], gp[N - 1]);
     uint32_t again = 0;
     for (int strip = w; strip < strips; strip += 4) {
         if (strip != w) take(strip);

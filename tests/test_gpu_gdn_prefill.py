@@ -278,3 +278,22 @@ def test_scores_that_overflow(rb, DK, lens, H, DV):
     o, S = rb.gdn_prefill(*(t.cuda() for t in (q, k, v, a, b)), starts.cuda(), ngroups=1)
     assert o.isfinite().all() and S.isfinite().all()
     check(o, S, q, k, v, a, b, starts, 1, 1.0, None)
+
+
+@pytest.mark.parametrize("DK,DV", [(64, 48), (128, 64), (256, 32)])
+@pytest.mark.parametrize("n,at", [(4, (0, 1, 2, 3)), (20, (3, 9, 15, 19)), (32, (0, 1, 30, 31)), (40, (2, 5, 37, 39)),
+                                  (64, (0, 31, 32, 63)), (150, (1, 60, 64, 149))])
+def test_strong_decays_keep_their_bits(rb, n, at, DK, DV):
+    """Four tokens that leave some 2^-25 of the state each, the others all, and nothing written: the state is its start times
+    the alphas.  In chunks the product comes from logarithms.  A token's is off by at most 2^-24 (an fp32 logarithm below 1/2,
+    two steps; the exponent is exact, and that of 1 is 0), which is ln 2 2^-24 of the product; each chunk adds the rounding of
+    the power's part (ln 2 2^-25), the power (one step, 2^-23) and the state's product (2^-24)."""
+    H = 8
+    q, k, v, a, b = gdn_inputs(n, n, H, H, DK, DV, BF, alpha=1.0, beta=0.0)
+    a[list(at)] = torch.exp2(-20 - 10 * torch.rand((4, H), generator=gen(n, 3)))
+    S0 = normal(gen(n, 4), 1, H, DV, DK)
+    o, S = rb.gdn_prefill(*(t.cuda() for t in (q, k, v, a, b)), starts_of([n]).cuda(), state=S0.cuda())
+    want = S0.double() * a.double().prod(0)[:, None, None]
+    bound = (4 * 0.694 + (n + 63) // 64 * (0.347 + 2 + 1)) * 2.0 ** -24
+    off = (S.cpu().double() - want).abs() / want.abs()
+    assert (off <= bound).all(), float(off.max()) / bound
