@@ -12,7 +12,7 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 constexpr int CHUNK = GDN_CHUNK;
 static_assert(CHUNK == 64, "tiles and fragments are laid out for 64 tokens");
 constexpr int FRAGS = 6;                       // (row tile, 32 tokens) pairs of a lower triangle: 0, 1, 2 x 2, 3 x 2
-constexpr int PIECE_P = 3 * FRAGS, PIECE_G = 5 * FRAGS;      // 1 KiB pieces: T (three terms), P (two), the g's
+constexpr int PIECE_P = 3 * FRAGS, PIECE_G = 5 * FRAGS;      // 1 KiB pieces: T (three terms), P (fp32), the g's
 static_assert((PIECE_G + 1) * 1024 == GDN_CHUNK_BYTES, "layout of a chunk in the workspace");
 
 // Token of row r of tile t (and d_k channel, of the state's tiles).
@@ -101,6 +101,22 @@ __device__ __forceinline__ Terms3 cut3(f32x4 lo, f32x4 hi)
 __device__ __forceinline__ Terms3 cut3(const float (&x)[8])
 {
     return cut3(f32x4{x[0], x[1], x[2], x[3]}, f32x4{x[4], x[5], x[6], x[7]});
+}
+
+// A product of two operands in terms, down to 2^-24: a sum for each size of term, the smallest joined first.
+__device__ __forceinline__ void product24(const bf16x8 (&x)[3], const bf16x8 (&y)[3], f32x4 (&sum)[3])
+{
+#pragma unroll
+    for (int e = 0; e < 3; ++e) sum[e] = mfma16x16x32bf16(x[0], y[e], sum[e]);
+    sum[0] = mfma16x16x32bf16(x[2], y[0], sum[0]);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) sum[2 - e] = mfma16x16x32bf16(x[1], y[e], sum[2 - e]);
+}
+__device__ __forceinline__ f32x4 product24(const Terms3& x, const Terms3& y)
+{
+    f32x4 sum[3] = {};
+    product24(x.t, y.t, sum);
+    return sum[0] + (sum[1] + sum[2]);
 }
 
 // Four rows of 16 values each, read across: lane (r, q) gets column r of the four rows that its group of 16 lanes points at,

@@ -13,9 +13,9 @@
 //   32 (t / 2) + 8 (r / 4) + 4 (t % 2) + r % 4,
 // which makes the eight values that a lane holds of tiles 2 s and 2 s + 1 consecutive ones: 32 s + 8 (l / 16) ...
 //
-// k and q are bf16 numbers; the fp32 operands are cut into bf16 terms of eight bits each (three hold all 24): S, X and U
-// in three, T in three and their products down to 2^-24, where they lead to the state; S and U in two, P in two and
-// products down to 2^-16 where they lead to o alone, which is rounded to 2^-9.  Sums are fp32.
+// k and q are bf16 numbers; the fp32 operands (S, X, U, T, P) are cut into three bf16 terms of eight bits each, which hold
+// all 24, and their products taken down to 2^-24.  Sums are fp32.  (o too: where new values take a large old state's place,
+// Q S^T and P U cancel, and terms of 16 bits would leave 2^-16 of the old state in a small o.)
 #include "gdn_chunk.hpp"
 
 #include <type_traits>
@@ -183,9 +183,8 @@ __global__ void __launch_bounds__(256, R == 256 ? 1 : 4) gdn_chunk_kernel(Prefil
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         p[x][k] = since(wi, pi, gw[j0 + 4 * x + k], gp[j0 + 4 * x + k]) * kq[e][x][k];
-                const Terms3 c = cut3(p[0], p[1]);
-                *reinterpret_cast<bf16x8*>(out + (PIECE_P + f) * 1024 + lane * 16) = c.t[0];
-                *reinterpret_cast<bf16x8*>(out + (PIECE_P + FRAGS + f) * 1024 + lane * 16) = c.t[1];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) *reinterpret_cast<f32x4*>(out + (PIECE_P + 2 * f + x) * 1024 + lane * 16) = p[x];
             }
             if (w == 1) {
                 float* g = reinterpret_cast<float*>(out + PIECE_G * 1024);
@@ -248,9 +247,9 @@ __global__ void __launch_bounds__(256, R == 256 ? 1 : 4) gdn_chunk_kernel(Prefil
 // asked for as soon as those of this one are used.  The unit that takes vector loads (some 25 cycles for each KiB) is as
 // busy as the matrix cores, so nothing is loaded twice: T, P and q as operands straight to registers, the g's and k through
 // LDS for all four waves (k also read across, as k^T), v eight bytes a lane and turned in LDS.  Bound by the chain of the three
-// exchanges: 512 chunks of one sequence by 32 heads 900 us, 1.8 us a chunk, of which the products of a wave are a fifth.
-// One strip a workgroup where that gives 512 or fewer, else two, which read T, P, q and k once for both (16 ragged prompts
-// 637 us with two strips, 898 with one).
+// exchanges: 512 chunks of one sequence by 32 heads 980 us, 1.9 us a chunk, of which the products of a wave are a fifth.
+// One strip a workgroup where that gives 512 or fewer, else two, which read T, P, q and k once for both (16 ragged prompts, with
+// the launch before: 818 us with two strips, 978 with one).
 // Returns whether there is such a head.
 template <int R, int NS>
 __device__ __forceinline__ bool state_of(const PrefillArgs& a, const uint8_t* ws, int slices, int i8)
@@ -258,12 +257,11 @@ __device__ __forceinline__ bool state_of(const PrefillArgs& a, const uint8_t* ws
     constexpr int M = R / 32, TW = R / 64, RB = R * 2;      // 32-channel steps, state tiles of a wave, bytes of a k row
     constexpr int CPR = RB / 16, KL = CPR / 4;              // 16-byte chunks of a row, of k that a lane brings to LDS
     __shared__ __attribute__((aligned(16))) uint8_t kbuf[CHUNK * RB];
-    __shared__ u32x4 sbuf[NS][M][3][64], xbuf[NS][2][3][64], dbuf[NS][2][3][64], ubuf[NS][2][2][64];
-    __shared__ __attribute__((aligned(16))) uint16_t turn[4][NS][16 * 16];      // v, then o, of a wave's tokens
+    __shared__ u32x4 sbuf[NS][M][3][64], xbuf[NS][2][3][64], dbuf[NS][2][3][64], ubuf[NS][2][3][64];
     __shared__ __attribute__((aligned(16))) float gbuf[3][CHUNK];
     const int tid = threadIdx.x, lane = tid & 63, w = uni(tid >> 6), r = lane & 15, q = lane >> 4;
     // Workgroups go to the 8 XCDs in turn.  The slices of a head read the same operands and go to one XCD; heads go to all,
-    // so that no XCD gets the longest sequences (16 ragged prompts, two for each XCD: 885 us against 637).
+    // so that no XCD gets the longest sequences (16 ragged prompts, two for each XCD: 874 us against 818).
     const int spread8 = a.most * a.H % 8 == 0;
     const int kh = spread8 ? i8 / (8 * slices) * 8 + i8 % 8 : i8 / slices, sl = spread8 ? i8 / 8 % slices : i8 % slices;
     const Turn which = turn_of(a, kh / a.H);
@@ -296,7 +294,10 @@ __device__ __forceinline__ bool state_of(const PrefillArgs& a, const uint8_t* ws
                      (tid + 256 * i) % CPR * 8;
     };
     const int tail = s.count - (nc - 1) * CHUNK;            // tokens of the last chunk
-    bf16x8 qf[M], tf[2][3], pf[2][2];
+    // where this wave turns v (before U is formed, in its place) and o (behind the third barrier, in X's)
+    uint16_t *turn_v = reinterpret_cast<uint16_t*>(ubuf) + w * NS * 256, *turn_o = reinterpret_cast<uint16_t*>(xbuf) + w * NS * 256;
+    bf16x8 qf[M], tf[2][3];
+    f32x4 pf[2][2];
     u32x4 kl[KL];
     u32x2 v[NS];
     float gl = 0.f;
@@ -339,7 +340,7 @@ __device__ __forceinline__ bool state_of(const PrefillArgs& a, const uint8_t* ws
             if (sg > sg_of) break;
             const int f = w < 2 ? w : 2 * w - 2 + sg;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) pf[sg][e] = *reinterpret_cast<const bf16x8*>(from + (PIECE_P + e * FRAGS + f) * 1024);
+            for (int e = 0; e < 2; ++e) pf[sg][e] = *reinterpret_cast<const f32x4*>(from + (PIECE_P + 2 * f + e) * 1024);
         }
     };
     // this wave's part of the state, for everyone
@@ -412,32 +413,29 @@ __device__ __forceinline__ bool state_of(const PrefillArgs& a, const uint8_t* ws
                 kf[m] = *reinterpret_cast<const bf16x8*>(kbuf + my_row * RB + (((4 * m + q) ^ (r & (CPR - 1))) * 16));
 #pragma unroll
             for (int n = 0; n < NS; ++n) {
-                f32x4 xe[3], oe[2];
-#pragma unroll
-                for (int e = 0; e < 3; ++e) xe[e] = f32x4{0.f, 0.f, 0.f, 0.f};
-                oe[0] = oe[1] = xe[0];
+                f32x4 xe[3] = {}, oe[3] = {};
 #pragma unroll
                 for (int m = 0; m < M; ++m)
 #pragma unroll
                     for (int e = 0; e < 3; ++e) {
                         const bf16x8 sc = __builtin_bit_cast(bf16x8, sbuf[n][m][e][lane]);
                         xe[e] = mfma16x16x32bf16(kf[m], sc, xe[e]);
-                        if (e < 2) oe[e] = mfma16x16x32bf16(qf[m], sc, oe[e]);
+                        oe[e] = mfma16x16x32bf16(qf[m], sc, oe[e]);
                     }
                 x[n] = xe[0] + (xe[1] + xe[2]);
-                o[n] = oe[0] + oe[1];
+                o[n] = oe[0] + (oe[1] + oe[2]);
             }
         }
         ask_rows(next);
         if (busy) {
             // X, and O as far as the state before the chunk goes
 #pragma unroll
-            for (int n = 0; n < NS; ++n) *reinterpret_cast<u32x2*>(&turn[w][n][lane * 4]) = v[n];
+            for (int n = 0; n < NS; ++n) *reinterpret_cast<u32x2*>(turn_v + n * 256 + lane * 4) = v[n];
             wave_lds_sync();
             const f32x4 gi = ld4(&gbuf[0][my_rows]), go = ld4(&gbuf[1][my_rows]);
 #pragma unroll
             for (int n = 0; n < NS; ++n) {
-                const u32x2 y = read_across(reinterpret_cast<const uint8_t*>(&turn[w][n][(4 * q + (r >> 2)) * 16 + (r & 3) * 4]));
+                const u32x2 y = read_across(reinterpret_cast<const uint8_t*>(turn_v + n * 256 + (4 * q + (r >> 2)) * 16 + (r & 3) * 4));
                 const float vf[4] = {__builtin_bit_cast(float, y.x << 16), __builtin_bit_cast(float, y.x & 0xffff0000u),
                                      __builtin_bit_cast(float, y.y << 16), __builtin_bit_cast(float, y.y & 0xffff0000u)};
 #pragma unroll
@@ -456,27 +454,22 @@ __device__ __forceinline__ bool state_of(const PrefillArgs& a, const uint8_t* ws
             // U = T X
 #pragma unroll
             for (int n = 0; n < NS; ++n) {
-                f32x4 ue[3];
-#pragma unroll
-                for (int e = 0; e < 3; ++e) ue[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+                f32x4 ue[3] = {};
 #pragma unroll
                 for (int sg = 0; sg < (both ? 2 : 1); ++sg) {
                     if (sg > sg_of) break;
                     bf16x8 xc[3];
 #pragma unroll
                     for (int e = 0; e < 3; ++e) xc[e] = __builtin_bit_cast(bf16x8, xbuf[n][sg][e][lane]);
-#pragma unroll
-                    for (int e = 0; e < 3; ++e) ue[e] = mfma16x16x32bf16(tf[sg][0], xc[e], ue[e]);
-                    ue[0] = mfma16x16x32bf16(tf[sg][2], xc[0], ue[0]);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) ue[2 - e] = mfma16x16x32bf16(tf[sg][1], xc[e], ue[2 - e]);
+                    product24(tf[sg], xc, ue);
                 }
                 const f32x4 u = ue[0] + (ue[1] + ue[2]);
                 const Cut t = cut(u), d = cut(u * ld4(&gbuf[2][my_rows]));
 #pragma unroll
-                for (int e = 0; e < 3; ++e) reinterpret_cast<u32x2*>(&dbuf[n][sg_of][e][lane])[half] = d.t[e];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) reinterpret_cast<u32x2*>(&ubuf[n][sg_of][e][lane])[half] = t.t[e];
+                for (int e = 0; e < 3; ++e) {
+                    reinterpret_cast<u32x2*>(&dbuf[n][sg_of][e][lane])[half] = d.t[e];
+                    reinterpret_cast<u32x2*>(&ubuf[n][sg_of][e][lane])[half] = t.t[e];
+                }
             }
         }
         ask_t(next);
@@ -497,20 +490,27 @@ __device__ __forceinline__ bool state_of(const PrefillArgs& a, const uint8_t* ws
                     for (int i = 0; i < TW; ++i) S[n][i] = mfma16x16x32bf16(kt[sg][i], uc, S[n][i]);
                 }
         if (busy) {
-            // O += P U
+            // O += P U (P's terms are cut here: fp32 are a third fewer bytes in the workspace and registers that wait)
+            f32x4 oe[NS][3];
 #pragma unroll
             for (int n = 0; n < NS; ++n) {
-                f32x4 oe[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
-#pragma unroll
-                for (int sg = 0; sg < (both ? 2 : 1); ++sg) {
-                    if (sg > sg_of) break;
-                    const bf16x8 hi = __builtin_bit_cast(bf16x8, ubuf[n][sg][0][lane]), lo = __builtin_bit_cast(bf16x8, ubuf[n][sg][1][lane]);
-                    o[n] = mfma16x16x32bf16(pf[sg][0], hi, o[n]);
-                    oe[0] = mfma16x16x32bf16(pf[sg][0], lo, oe[0]);
-                    oe[1] = mfma16x16x32bf16(pf[sg][1], hi, oe[1]);
-                }
-                o[n] += oe[0] + oe[1];
+                oe[n][0] = o[n];
+                oe[n][1] = oe[n][2] = f32x4{0.f, 0.f, 0.f, 0.f};
             }
+#pragma unroll
+            for (int sg = 0; sg < (both ? 2 : 1); ++sg) {
+                if (sg > sg_of) break;
+                const Terms3 p = cut3(pf[sg][0], pf[sg][1]);
+#pragma unroll
+                for (int n = 0; n < NS; ++n) {
+                    bf16x8 uc[3];
+#pragma unroll
+                    for (int e = 0; e < 3; ++e) uc[e] = __builtin_bit_cast(bf16x8, ubuf[n][sg][e][lane]);
+                    product24(p.t, uc, oe[n]);
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NS; ++n) o[n] = oe[n][0] + (oe[n][1] + oe[n][2]);
         }
         tell_state();
         keep_k();
@@ -525,13 +525,13 @@ __device__ __forceinline__ bool state_of(const PrefillArgs& a, const uint8_t* ws
 #pragma unroll
             for (int n = 0; n < NS; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) turn[w][n][(4 * q + i) * 16 + r] = f32_to_bf16_bits(o[n][i]);
+                for (int i = 0; i < 4; ++i) turn_o[n * 256 + (4 * q + i) * 16 + r] = f32_to_bf16_bits(o[n][i]);
             wave_lds_sync();
             const int row = tile_row(w, lane >> 2), left = s.count - c * CHUNK;
             uint16_t* op = static_cast<uint16_t*>(a.o) + ((size_t)(s.first + c * CHUNK + row) * a.H + h) * a.C + (lane & 3) * 4;
 #pragma unroll
             for (int n = 0; n < NS; ++n) {
-                const u32x2 y = *reinterpret_cast<const u32x2*>(&turn[w][n][lane * 4]);
+                const u32x2 y = *reinterpret_cast<const u32x2*>(turn_o + n * 256 + lane * 4);
                 if (row < left && strip0 + n < strips) *reinterpret_cast<u32x2*>(op + col[n]) = y;
             }
         }

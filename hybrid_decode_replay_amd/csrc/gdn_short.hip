@@ -142,13 +142,11 @@ __global__ void __launch_bounds__(256, R == 256 ? 1 : 2) gdn_short_kernel(Prefil
     // K S^T and Q S^T of a strip (a sum for each term: the products of one sum would wait for one another)
     f32x4 x[2], o[2];
     auto read_out = [&]() {
-        f32x4 xe[2][3], oe[2][2];
+        f32x4 xe[2][3], oe[2][3];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int e = 0; e < 3; ++e) xe[t][e] = f32x4{0.f, 0.f, 0.f, 0.f};
-            oe[t][0] = oe[t][1] = xe[t][0];
-        }
+            for (int e = 0; e < 3; ++e) xe[t][e] = oe[t][e] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int m = 0; m < M; ++m) {
             const Terms3 sc = cut3(S[2 * m], S[2 * m + 1]);
@@ -159,14 +157,14 @@ __global__ void __launch_bounds__(256, R == 256 ? 1 : 2) gdn_short_kernel(Prefil
 #pragma unroll
                 for (int e = 0; e < 3; ++e) {
                     xe[t][e] = mfma16x16x32bf16(kf, sc.t[e], xe[t][e]);
-                    if (e < 2) oe[t][e] = mfma16x16x32bf16(qf, sc.t[e], oe[t][e]);
+                    oe[t][e] = mfma16x16x32bf16(qf, sc.t[e], oe[t][e]);
                 }
             }
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             x[t] = xe[t][0] + (xe[t][1] + xe[t][2]);
-            o[t] = oe[t][0] + oe[t][1];
+            o[t] = oe[t][0] + (oe[t][1] + oe[t][2]);
         }
     };
     u32x2 v[2];
@@ -182,7 +180,7 @@ __global__ void __launch_bounds__(256, R == 256 ? 1 : 2) gdn_short_kernel(Prefil
     lds_barrier();
     if (w >= strips) return;
     Terms3 tf[2];
-    bf16x8 pf[2][2];
+    Terms3 pf[2];
     f32x4 gi[2], gd[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -191,9 +189,7 @@ __global__ void __launch_bounds__(256, R == 256 ? 1 : 2) gdn_short_kernel(Prefil
         const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
         const f32x4 b0 = ld4(bt + j0), b1 = ld4(bt + j0 + 4);
         tf[t] = cut3(lower ? ld4(tm + i * LD + j0) * b0 : zero, lower ? ld4(tm + i * LD + j0 + 4) * b1 : zero);
-        const Terms3 p = cut3(lower ? ld4(pm + i * LD + j0) : zero, lower ? ld4(pm + i * LD + j0 + 4) : zero);
-        pf[t][0] = p.t[0];
-        pf[t][1] = p.t[1];
+        pf[t] = cut3(lower ? ld4(pm + i * LD + j0) : zero, lower ? ld4(pm + i * LD + j0 + 4) : zero);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int row = tile_row(t, 4 * q + e);
@@ -223,22 +219,10 @@ __global__ void __launch_bounds__(256, R == 256 ? 1 : 2) gdn_short_kernel(Prefil
         const Terms3 xc = cut3(x[0], x[1]);
         f32x4 u[2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            f32x4 ue[3];
-#pragma unroll
-            for (int e = 0; e < 3; ++e) ue[e] = mfma16x16x32bf16(tf[t].t[0], xc.t[e], f32x4{0.f, 0.f, 0.f, 0.f});
-            ue[0] = mfma16x16x32bf16(tf[t].t[2], xc.t[0], ue[0]);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) ue[2 - e] = mfma16x16x32bf16(tf[t].t[1], xc.t[e], ue[2 - e]);
-            u[t] = ue[0] + (ue[1] + ue[2]);
-        }
+        for (int t = 0; t < 2; ++t) u[t] = product24(tf[t], xc);
         const Terms3 uc = cut3(u[0], u[1]), dc = cut3(u[0] * gd[0], u[1] * gd[1]);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            o[t] = mfma16x16x32bf16(pf[t][0], uc.t[0], o[t]);
-            o[t] = mfma16x16x32bf16(pf[t][0], uc.t[1], o[t]);
-            o[t] = mfma16x16x32bf16(pf[t][1], uc.t[0], o[t]);
-        }
+        for (int t = 0; t < 2; ++t) o[t] += product24(pf[t], uc);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const int row = 8 * q + (r >> 2), ch = 4 * (t >> 1) + (r & 3), c8 = (t & 1) * 8;

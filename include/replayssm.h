@@ -651,9 +651,9 @@ replay_status replay_linear_fp8(const replay_linear_fp8_args *args, void *stream
  * means zeros, and S_out (which may be S_in, or NULL) is what replay_load_slots
  * takes.  Sums and states are held in fp32.  fp32 inputs, and d_k below 64, are
  * taken token by token.  bf16 with d_k from 64 on goes in chunks of 64 tokens on
- * the matrix cores: their fp32 operands enter as bf16 terms that hold 24 bits
- * where they lead to the state and 16 where they lead to o alone.  An infinity or
- * NaN reaches what follows it in its head and nothing else, in either way. */
+ * the matrix cores: their fp32 operands enter as bf16 terms that hold 24 bits.
+ * An infinity or NaN reaches what follows it in its head and nothing else, in
+ * either way. */
 typedef struct {
     int32_t abi_version;  /* REPLAY_ABI_VERSION                                    */
     int32_t io_dtype;     /* REPLAY_BF16 | REPLAY_F32: q, k, v, o                  */

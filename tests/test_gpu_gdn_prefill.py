@@ -297,3 +297,63 @@ def test_strong_decays_keep_their_bits(rb, n, at, DK, DV):
     bound = (4 * 0.694 + (n + 63) // 64 * (0.347 + 2 + 1)) * 2.0 ** -24
     off = (S.cpu().double() - want).abs() / want.abs()
     assert (off <= bound).all(), float(off.max()) / bound
+
+
+WAYS = [([30], 2, 48), ([32], 1, 16), ([64], 2, 48), ([150, 7], 2, 64), ([33], 1, 16), ([70, 0, 65, 100, 64], 32, 80),
+        ([40] + [9] * 39, 32, 48)]
+
+
+def whole_numbers(lens, H, DK, DV, size, seed):
+    """Keys and queries of one channel each (half the queries are their token's key), whole numbers up to `size` in v and
+    some 2^23 in the states: all that is formed of them is a whole number of at most 24 bits."""
+    rows, g = sum(lens), gen(seed, DK, DV, H)
+    hot = lambda i: torch.zeros((rows, H, DK)).scatter_(2, i[..., None], 1.0).flatten(1).to(BF)  # noqa: E731
+    ki = torch.randint(0, DK, (rows, H), generator=g)
+    qi = torch.where(torch.rand((rows, H), generator=g) < 0.5, ki, torch.randint(0, DK, (rows, H), generator=g))
+    v = torch.randint(-size, size + 1, (rows, H * DV), generator=g).to(BF)
+    S0 = torch.randint(-2 ** 23 + 1024, 2 ** 23 - 1024, (len(lens), H, DV, DK), generator=g).float()
+    return hot(qi), hot(ki), v, S0
+
+
+def check_exact(rb, lens, H, q, k, v, a, b, scale, S0):
+    starts = starts_of(lens)
+    o, S = rb.gdn_prefill(*(t.cuda() for t in (q, k, v, a, b)), starts.cuda(), scale=scale, state=S0.cuda())
+    o, S = o.cpu(), S.cpu()
+    for i, (lo, hi) in enumerate(zip(starts.tolist(), starts.tolist()[1:])):
+        T = S0[i].double().clone()
+        for t in range(lo, hi):
+            kt, qt, vt = (x[t].double().view(H, -1) for x in (k, q, v))
+            T = T * a[t, :, None, None].double()
+            u = b[t, :, None].double() * (vt - (T @ kt[..., None])[..., 0])
+            T = T + u[..., None] * kt[:, None]
+            want = (scale * (T @ qt[..., None])[..., 0]).float()
+            assert torch.equal(o[t].view(H, -1), want.to(BF)), (i, t - lo)
+        assert torch.equal(S[i].double(), T), i
+
+
+@pytest.mark.parametrize("DK", [64, 128, 256])
+@pytest.mark.parametrize("lens,H,DV", WAYS)
+def test_whole_numbers(rb, DK, lens, H, DV):
+    """Small values take the place of 24-bit ones: every step is exact in fp32, so states and outputs are, in chunks too.
+    (Of S and U in 16 bits, an output that is v - (24 bits) + (24 bits) would be off by up to 2^7.)"""
+    q, k, v, S0 = whole_numbers(lens, H, DK, DV, 255, 1)
+    a = torch.ones((sum(lens), H))
+    check_exact(rb, lens, H, q, k, v, a, torch.ones_like(a), 1.0, S0)
+
+
+@pytest.mark.parametrize("DK", [64, 128, 256])
+@pytest.mark.parametrize("lens,H,DV", WAYS)
+def test_factors_of_many_bits(rb, DK, lens, H, DV):
+    """beta, then scale, of 1 + 2^-9 + 2^-20 (three terms of eight bits) on numbers of three bits: the triangle's inverse and
+    the masked scores hold 24 bits."""
+    rows, g = sum(lens), gen(5, DK)
+    order = torch.stack([torch.randperm(64, generator=g) for _ in range(H)], 1)         # no key twice in a chunk
+    since = torch.cat([torch.arange(n) % 64 for n in lens])
+    hot = torch.zeros((rows, H, DK)).scatter_(2, order[since][..., None], 1.0).flatten(1).to(BF)
+    S0 = torch.randint(0, 4, (len(lens), H, DV, DK), generator=g).float()
+    v = torch.randint(0, 4, (rows, H * DV), generator=g).to(BF)
+    a, c = torch.ones((rows, H)), 1 + 2.0 ** -9 + 2.0 ** -20
+    if max(lens) <= 64:
+        check_exact(rb, lens, H, hot, hot, v, a, c * a, 1.0, S0)
+    # (what replaces 5 2^10 is 0: scale s - scale s, each of 24 bits)
+    check_exact(rb, lens, H, hot, hot, torch.zeros_like(v), a, a, c, 5 * 2.0 ** 10 * S0.clamp(max=1))
