@@ -357,3 +357,98 @@ def test_factors_of_many_bits(rb, DK, lens, H, DV):
         check_exact(rb, lens, H, hot, hot, v, a, c * a, 1.0, S0)
     # (what replaces 5 2^10 is 0: scale s - scale s, each of 24 bits)
     check_exact(rb, lens, H, hot, hot, torch.zeros_like(v), a, a, c, 5 * 2.0 ** 10 * S0.clamp(max=1))
+
+
+def way(rb, lens, H, DK, DV):
+    """Which launches a call takes: "short", "chunks" or "mixed", and whether a workgroup of the chunks has two strips.  From
+    the workspace, which counts the sequences that the chunks take at most (where that is all of them in either case: a mean of
+    33 tokens and more: by the host's rule, a mean below 64 of 1024 sequence-heads and more)."""
+    def units(rows, nseq):
+        z = lambda w, t=BF: torch.empty((rows, w), dtype=t, device="cuda")  # noqa: E731
+        return rb.gdn_prefill_workspace(z(H * DK), z(H * DK), z(H * DV), z(H, F32), z(H, F32),
+                                        torch.empty(nseq + 1, dtype=torch.int32, device="cuda"))
+    rows, nseq = sum(lens), len(lens)
+    need = units(rows, nseq)
+    if need == 0:
+        return "short", False
+    most = need * 2 // units(64, 1) - rows // 64
+    few = min(nseq, rows // 33)
+    assert most in (few, nseq)
+    mixed = most < nseq if few < nseq else rows < 64 * nseq and nseq * H >= 1024
+    return "mixed" if mixed else "chunks", DK < 256 and most * H * (DV // 16) > 512
+
+
+@pytest.mark.parametrize("lens,H,G,DV", [([70, 0, 130, 64, 90], 32, 16, 64), ([100, 65, 33, 0, 200], 36, 9, 48),
+                                         ([40, 90, 0, 64, 129, 100, 63], 15, 5, 80), ([30] * 30 + [0, 100, 33, 65, 1, 32] * 6, 2, 1, 64)])
+@pytest.mark.parametrize("DK", [64, 128])
+def test_two_strips_a_workgroup(rb, DK, lens, H, G, DV):
+    """Batches of ordinary prompts: two strips a workgroup (the last one's alone where they are odd), the longest first up to
+    64 sequences, heads spread over the chip or not."""
+    assert way(rb, lens, H, DK, DV) == ("chunks", True)
+    run(rb, lens, H, G, DK, DV, BF, seed=len(lens))
+
+
+BAD = [([15, 15], 2, 96, "short", False), ([32], 2, 48, "short", False), ([9, 1, 20], 2, 256, "short", False),
+       ([70, 0, 80, 66], 4, 48, "chunks", False), ([70, 0, 130, 64, 90], 44, 48, "chunks", True),
+       ([9] * 38 + [40, 100], 32, 48, "mixed", True)]
+
+
+@pytest.mark.parametrize("lens,H,DV,by,two", BAD)
+@pytest.mark.parametrize("DK", [64, 128, 256])
+@pytest.mark.parametrize("what", ["q", "k", "v", "alpha", "state"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_bad_values_in_every_way(rb, DK, lens, H, DV, by, two, what, value):
+    """An infinity or NaN in one head of the longest sequence (and of the shortest with rows, in a mixed call), states in place:
+    what follows it in its head, and nothing else."""
+    assert way(rb, lens, H, DK, DV) == (by, two and DK < 256)
+    rows, starts = sum(lens), starts_of(lens)
+    q, k, v, a, b = gdn_inputs(31, rows, H, H, DK, DV, BF)
+    S0 = normal(gen(9), len(lens), H, DV, DK, std=0.3)
+    hit = {lens.index(max(lens))} | ({0} if by == "mixed" else set())
+    h, ch = H - 1, DV - 11                     # (the last strip)
+    args, state = [t.clone() for t in (q, k, v, a, b)], S0.clone()
+    for i in hit:
+        j = int(starts[i]) + lens[i] * 2 // 3
+        if what == "state":
+            state[i, h, ch, 3] = value
+        else:
+            args["q k v alpha".split().index(what)][j, {"q": h * DK + 5, "k": h * DK + 5, "v": h * DV + ch, "alpha": h}[what]] = value
+    state = state.cuda()
+    o, S = rb.gdn_prefill(*(t.cuda() for t in args), starts.cuda(), state=state, state_out=state)
+    near = {i for x in hit for i in (x - 1, x + 1) if 0 <= i < len(lens)} - hit
+    check(o, S, q, k, v, a, b, starts, H, 1.0, S0, which=near | ({len(lens) - 1} - hit))
+    for i in hit:
+        lo, n = int(starts[i]), lens[i]
+        at = slice(lo, lo + n)
+        for one in (0, h - 1, h):
+            take = [t[at].view(n, H, -1)[:, one] for t in (q, k, v)] + [t[at, one:one + 1] for t in (a, b)]
+            wo, wS, bo, bS = gdn_plain(*take, 1, 1.0, S0[i, one:one + 1])
+            got = o[at].cpu().double().view(n, H, DV)[:, one]
+            good = (got - wo[:, 0]).abs() <= bo[:, 0] + HALF[BF] * (wo[:, 0].abs() + bo[:, 0])
+            fine = (S[i, one].cpu().double() - wS[0]).norm(dim=-1) <= bS[0] + 2.0 ** -24 * wS[0].norm(dim=-1)
+            since = 0 if what == "state" else n * 2 // 3
+            if one != h:
+                assert good.all() and fine.all(), (i, one)
+            elif what in ("v", "state"):
+                rest = torch.arange(DV) != ch
+                assert good[:, rest].all() and fine[rest].all() and good[:since].all(), i
+                assert not got[since:, ch].isfinite().any() and not S[i, h, ch].isfinite().all()
+            elif what == "q":
+                rest = torch.arange(n) != since
+                assert good[rest].all() and fine.all() and not got[since].isfinite().any(), i
+            else:
+                assert good[:since].all() and not got[since:].isfinite().any() and not S[i, h].isfinite().all(-1).any(), i
+
+
+def test_workgroups_go_on_after_a_bad_value(rb):
+    """More heads of long sequences than start at a time: a workgroup that has gone over its first head once more takes its
+    next one as if nothing had been."""
+    H, DK, DV, lens = 64, 64, 80, [40] * 14 + [3] * 10
+    assert way(rb, lens, H, DK, DV) == ("mixed", True)
+    q, k, v, a, b = gdn_inputs(37, sum(lens), H, 1, DK, DV, BF)
+    starts, bad = starts_of(lens), v.clone()
+    bad[[25, 65, 110], ::16] = float("nan")
+    o, S = rb.gdn_prefill(*(t.cuda() for t in (q, k, bad, a, b)), starts.cuda(), ngroups=1)
+    check(o, S, q, k, v, a, b, starts, 1, 1.0, None, which=[3, 9, 10, 11, 12, 13, 14, 23])
+    hit = torch.arange(H * DV) % 16 == 0
+    assert not o[25:40].cpu()[:, hit].isfinite().any() and o[:25].isfinite().all() and o[:120].cpu()[:, ~hit].isfinite().all()
