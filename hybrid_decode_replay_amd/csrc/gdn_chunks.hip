@@ -37,6 +37,7 @@ __global__ void __launch_bounds__(256, R == 256 ? 1 : 4) gdn_chunk_kernel(Prefil
     __shared__ __attribute__((aligned(16))) uint8_t both[ROWS > 2 * MAT ? ROWS : 2 * MAT];    // k and q, then T and A
     __shared__ __attribute__((aligned(16))) int gw[CHUNK];
     __shared__ __attribute__((aligned(16))) float gp[CHUNK], bt[CHUNK];
+    static_assert((R == 256 ? 2 : 4) * (sizeof both + sizeof gw + sizeof gp + sizeof bt) <= 160 * 1024, "workgroups of a CU");
     float *tm = reinterpret_cast<float*>(both), *am = reinterpret_cast<float*>(both + MAT);
     // 16-byte chunks of a row are exchanged by this, so that 16 rows in order, and in a tile's order, are spread over the banks
     auto key = [](int row) { return ((row & 3) | (row >> 1 & 4) | (((row << 1) ^ (row >> 1)) & 8)) & (CPR - 1); };
@@ -259,6 +260,7 @@ __device__ __forceinline__ bool state_of(const PrefillArgs& a, const uint8_t* ws
     __shared__ __attribute__((aligned(16))) uint8_t kbuf[CHUNK * RB];
     __shared__ u32x4 sbuf[NS][M][3][64], xbuf[NS][2][3][64], dbuf[NS][2][3][64], ubuf[NS][2][3][64];
     __shared__ __attribute__((aligned(16))) float gbuf[3][CHUNK];
+    static_assert(2 * (sizeof kbuf + sizeof sbuf + sizeof xbuf + sizeof dbuf + sizeof ubuf + sizeof gbuf) <= 160 * 1024, "workgroups of a CU");
     const int tid = threadIdx.x, lane = tid & 63, w = uni(tid >> 6), r = lane & 15, q = lane >> 4;
     // Workgroups go to the 8 XCDs in turn.  The slices of a head read the same operands and go to one XCD; heads go to all,
     // so that no XCD gets the longest sequences (16 ragged prompts, two for each XCD: 874 us against 818).

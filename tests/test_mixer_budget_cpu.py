@@ -37,3 +37,11 @@ def test_mixer_kernels_use_no_scratch_and_leave_room_for_their_waves(tmp_path):
     bad = [f"{n}: {scratch} B/lane scratch, {waves} waves/SIMD (needs {waves_needed(n)})" for n, scratch, waves in found
            if scratch > 0 or waves < waves_needed(n)]
     assert not bad, "\n".join(bad)
+
+
+@pytest.mark.skipif(not (os.path.exists(hb.HIPCC) or shutil.which(hb.HIPCC)), reason="hipcc not available")
+def test_four_workgroups_of_the_chunk_kernel_fit_a_cu(tmp_path):
+    """Below d_k 256 its launch bounds, and the time of its launch, count on four waves a SIMD; three would pass the test above."""
+    found = {n: waves for n, _, waves in _kernels(_remarks("gdn_chunks.hip", str(tmp_path))) if "gdn_chunk_kernel" in n}
+    assert len(found) == 3
+    assert all(waves >= 4 for n, waves in found.items() if "Li256E" not in n), found
