@@ -874,6 +874,12 @@ def _codes():
     return _CODES
 
 
+def _sizes(where, *sizes):
+    """Refuses sizes that the library's 32-bit ones would cut."""
+    if max(sizes) >= 1 << 31:
+        raise ValueError(f"{where}: sizes must be below 2^31, got {max(sizes)}")
+
+
 def norm(x, weight=None, heads=1, eps=1e-6, res=None, res_out=None, y=None, y_scale=None, out_dtype=None):
     """Root-mean-square norm (replay_norm) of x [rows][heads*n] (any row stride), each head's n channels by
     themselves; res (same shape) is added first and, with res_out, the sum written there (res_out may be res).
@@ -885,6 +891,7 @@ def norm(x, weight=None, heads=1, eps=1e-6, res=None, res_out=None, y=None, y_sc
     if len(shape) != 2 or heads < 1 or shape[1] % heads != 0:
         raise ValueError("x must be [rows][heads * n]")
     rows, width = shape
+    _sizes("norm", rows, width)
     if y is None:
         y = torch.empty(shape, dtype=out_dtype or io, device=dev)
     kind = y.dtype
@@ -919,6 +926,7 @@ def linear_fp8(x, x_scale, w, w_scale, y=None, out_dtype=None):
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x must be [m][k] and w [n][k]")
     (m, k), n = x.shape, w.shape[0]
+    _sizes("linear_fp8", m, k, n)
     if y is None:
         y = torch.empty((m, n), dtype=out_dtype or torch.bfloat16, device=dev)
     kind = y.dtype
@@ -942,6 +950,7 @@ def _prefill_args(q, k, v, alpha, beta, starts, ngroups, scale):
     G = H if ngroups is None else ngroups
     if G < 1 or q.shape[1] % G != 0 or H < 1 or v.shape[1] % H != 0:
         raise ValueError("q and k must be [rows][ngroups * d_k] and v [rows][heads * d_v]")
+    _sizes("gdn_prefill", rows, H, q.shape[1], v.shape[1], starts.shape[0])
     a = GDNPrefillArgs(ABI_VERSION, _codes().get(io, NONE), H, G, v.shape[1] // H, q.shape[1] // G,
                        starts.shape[0] - 1, rows, scale)
     a.starts = _addr(starts, dev, torch.int32, "starts")

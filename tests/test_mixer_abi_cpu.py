@@ -128,3 +128,27 @@ def test_structures_match_the_header():
         subprocess.run(["gcc", "-I", os.path.dirname(b.HEADER), "-o", os.path.join(d, "s"), os.path.join(d, "s.c")], check=True)
         out = subprocess.run([os.path.join(d, "s")], capture_output=True, text=True, check=True).stdout
     assert [int(x) for x in out.split()] == [ctypes.sizeof(t) for t in (b.NormArgs, b.LinearFP8Args, b.GDNPrefillArgs)]
+
+
+def test_the_binding_refuses_sizes_past_32_bits(monkeypatch):
+    """Sizes that would arrive in the library cut to 32 bits (2^32 + 1 rows as one row, with no error)."""
+    torch = pytest.importorskip("torch")
+    b = rb()
+    monkeypatch.setattr(b, "_on_device", lambda device, what="": device)
+    monkeypatch.setattr(b, "_launch", lambda *a: pytest.fail("launched"))
+    t = lambda *s, dtype=torch.bfloat16: torch.empty(s, dtype=dtype, device="meta")  # noqa: E731
+    many, f32, e4m3 = (1 << 32) + 1, torch.float32, torch.float8_e4m3fn
+    for x in (t(many, 8), t(1 << 31, 8), t(1, (1 << 32) + 128)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            b.norm(x)
+    for m, k, n in ((many, 128, 8), (1, 128, many), (2, (1 << 32) + 128, 8)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            b.linear_fp8(t(m, k, dtype=e4m3), t(m, k // 128, dtype=f32), t(n, k, dtype=e4m3), t(-(-n // 128), k // 128, dtype=f32))
+    for rows, H, dk, dv, starts in ((many, 1, 16, 16, 2), (4, 1, 16, 16, many), (1, many, 1, 1, 2), (1, 1, (1 << 32) + 16, 16, 2),
+                                    (1, 1, 16, (1 << 32) + 16, 2)):
+        args = (t(rows, H * dk), t(rows, H * dk), t(rows, H * dv), t(rows, H, dtype=f32), t(rows, H, dtype=f32),
+                t(starts, dtype=torch.int32))
+        with pytest.raises(ValueError, match="2\\^31"):
+            b.gdn_prefill(*args)
+        with pytest.raises(ValueError, match="2\\^31"):
+            b.gdn_prefill_workspace(*args)
