@@ -70,17 +70,37 @@ __global__ void __launch_bounds__(256) norm_kernel(NormArgs a)
         if (a.sum && live && c < chunks)
             __builtin_nontemporal_store(kv_pack8<IO>(s[i]), reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.sum) + out) + c);
     }
-    if constexpr (LPR <= 64) {
-        ss = group_sum<LPR>(ss);
-    } else {
-        __shared__ float part[4];
-        ss = group_sum<64>(ss);
-        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = ss;
-        __syncthreads();
-        ss = (part[0] + part[1]) + (part[2] + part[3]);
+    auto run_sum = [](float v) {
+        if constexpr (LPR <= 64) {
+            return group_sum<LPR>(v);
+        } else {
+            __shared__ float part[4];
+            v = group_sum<64>(v);
+            if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+            __syncthreads();
+            return (part[0] + part[1]) + (part[2] + part[3]);
+        }
+    };
+    float mean = __builtin_fmaf(run_sum(ss), a.inv_n, a.eps);
+    // A run whose squares left the fp32 range (their sum is an infinity, or so small that squares lost bits and eps does not
+    // cover it) once more, times a power of two.  (Runs beside it in a wave take part with 1, so that no lane is apart.)
+    constexpr uint32_t LOW = 27u << 23, END = 0x7f800000u;         // 2^-100, infinity
+    const bool out_of_range = __builtin_bit_cast(uint32_t, mean) - LOW >= END - LOW;
+    if (__builtin_expect(__ballot(out_of_range) != 0, 0)) {
+        const float p = !out_of_range ? 1.f : mean < 1.f ? 0x1p100f : 0x1p-80f;
+        ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                s[i][j] *= p;
+                ss = __builtin_fmaf(s[i][j], s[i][j], ss);
+            }
+        if constexpr (LPR > 64) __syncthreads();
+        mean = __builtin_fmaf(run_sum(ss), a.inv_n, a.eps * p * p);
     }
     // (the square root and the division are rounded to fp32 each: E4M3 scales are fp32 outputs)
-    const float inv = 1.f / __builtin_sqrtf(__builtin_fmaf(ss, a.inv_n, a.eps));
+    const float inv = 1.f / __builtin_sqrtf(mean);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         const int c = lane + i * LPR;

@@ -584,8 +584,8 @@ replay_status replay_kv_attention(const replay_kv_layer *layer, const replay_kv_
  * nearest even.  y_dtype = REPLAY_FP8_E4M3: for each 128 channels
  *   scale = max(largest |y| / 448, 2^-126),  code = E4M3 nearest to y / scale,
  * ties to even; a NaN becomes 0x7f and is left out of its group's scale, an
- * infinite y counts as the largest fp32 number.  Squares are summed in fp32, so
- * magnitudes of s past 2^63 overflow (y = 0). */
+ * infinite y counts as the largest fp32 number.  Squares are summed in fp32, of a
+ * run whose squares are out of its range times a power of two. */
 typedef struct {
     int32_t abi_version;  /* REPLAY_ABI_VERSION                                    */
     int32_t io_dtype;     /* REPLAY_BF16 | REPLAY_F16: x, res, weight, sum         */

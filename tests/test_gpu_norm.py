@@ -175,3 +175,24 @@ def test_another_stream_and_a_graph(rb):
         graph.replay()
         want, ws = rb.norm(x, w, out_dtype=E4M3)
         assert torch.equal(y.view(torch.uint8), want.view(torch.uint8)) and torch.equal(scale, ws)
+
+
+@pytest.mark.parametrize("n,heads", [(72, 3), (128, 5), (256, 3), (512, 1), (1024, 1), (2048, 1), (4096, 1), (8192, 1), (16384, 1)])
+@pytest.mark.parametrize("out", [None, E4M3])
+def test_squares_out_of_range(rb, n, heads, out):
+    """Runs of 2^-126 to 2^126 beside ordinary ones, eps 0: their squares are out of the range of fp32."""
+    if out is not None and n % 128:
+        pytest.skip("E4M3 goes by groups of 128")
+    g = gen(n, heads, 6)
+    powers = [0, -126, -90, -75, -64, -55, -50, -45, 0, 55, 60, 64, 100, 124, 0]
+    x = normal(g, len(powers), heads * n)
+    x = (x * torch.exp2(torch.tensor(powers, dtype=torch.float32))[:, None]).to(torch.bfloat16)
+    if heads > 1:                                     # (heads of a row differ too)
+        x[:, n:2 * n] = normal(g, len(powers), n).to(torch.bfloat16)
+    w = normal(g, n, dtype=torch.bfloat16)
+    y, scale = rb.norm(x.cuda(), w.cuda(), heads=heads, eps=0.0, out_dtype=out)
+    check(y, scale, None, x, w, heads, 0.0, None)
+    res = x.flip(0).contiguous()
+    total = torch.empty_like(x, device="cuda")
+    y, scale = rb.norm(x.cuda(), w.cuda(), heads=heads, eps=1e-30, res=res.cuda(), res_out=total, out_dtype=out)
+    check(y, scale, total, x, w, heads, 1e-30, res)
