@@ -27,7 +27,8 @@ namespace rs {
 // lower triangle of K K^T, and K Q^T in tiles whose rows are ordered as above (a lane then holds the eight values of P that it
 // stores), stay in registers for the group's heads.  Each head's triangle is inverted in blocks of 16: the four diagonal
 // blocks by forward substitution in one wave (a lane a column; the others form and store P meanwhile), then the blocks below
-// them column by column, a wave each, in fp32 matrix products.
+// them column by column, a wave each, in fp32 matrix products.  Bound by its bytes where chunks are many (16 ragged prompts by
+// 32 heads read and write 916 MB in 156 us, 5.9 TB/s).
 template <int R>
 __global__ void __launch_bounds__(256, R == 256 ? 1 : 4) gdn_chunk_kernel(PrefillArgs a, uint8_t* ws)
 {

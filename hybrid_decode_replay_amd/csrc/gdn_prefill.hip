@@ -4,7 +4,7 @@
 //
 // Rows of S (channels of d_v) do not depend on one another: 16 lanes hold a row's d_k values in registers, a wave 4 RPL
 // rows.  The inputs of the next token are on their way while one is computed.  Bound by that chain of a token: 0.6 us each (bf16,
-// 32 heads of 128 x 128: 32768 tokens of one sequence 20.3 ms, where chunks on the matrix cores take 1.1), so it is the way of
+// 32 heads of 128 x 128: 32768 tokens of one sequence 20.3 ms, where chunks on the matrix cores take 1.2), so it is the way of
 // what the chunks do not take: fp32 inputs, whose products would need three times the terms, and d_k below 64.
 #include "common.hpp"
 #include "mixer.hpp"

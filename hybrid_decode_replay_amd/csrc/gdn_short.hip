@@ -2,7 +2,7 @@
 //
 // The chunk's algebra of gdn_chunks.hip in one launch: a workgroup takes a head, forms T and P of its tokens in LDS, and each
 // of its four waves then takes strips of 16 d_v columns of the state one after the other, from load to store, the next one on
-// its way: no barrier, no workspace.  Bound by the states' bytes: 192 pieces of 1 to 33 tokens by 32 heads (916 MB) 188 us.
+// its way: no barrier, no workspace.  Bound by the states' bytes: 192 pieces of 1 to 33 tokens by 32 heads (890 MB) 199 us.
 #include "gdn_chunk.hpp"
 
 namespace rs {

@@ -402,10 +402,11 @@ bool prefill_in_chunks(const replay_gdn_prefill_args* a)
 }
 
 // The lengths are on the device: of few tokens a sequence on average, sequences of up to GDN_SHORT get a launch of their own
-// beside the chunks (which leaves the others alone, and they these).  With it and without it, in us, 32 heads of 128 x 128:
-// 192 sequences of 18 tokens on average 246 and 481, of 46 588 and 631, of 63 707 and 728, of 92 877 and 874; 32 of 44 114 and
-// 116, of 67 142 and 137.  Where the heads of all sequences do not fill the chip the launch is one more in a chain: 16 of 14
-// tokens 27 and 45, of 22 47 and 48, of 50 69 and 58; 4 of 20 20 and 19, of 26 31 and 21.
+// beside the chunks (which leaves the others alone, and they these).  With it and without it, in us, 32 heads of 128 x 128 with
+// states, lengths spread evenly from 1 on: 192 sequences of 18 tokens on average 260 and 431, of 46 530 and 568, of 63 627 and
+// 638, of 92 790 and 770; 32 of 44 112 and 120, of 67 138 and 135.  Where the heads of all sequences do not fill the chip the
+// launch is one more in a chain: 16 of 14 tokens 27 and 44, of 22 43 and 48, of 50 65 and 59; 4 of 20 28 and 19, of 26 31 and
+// 20.
 bool prefill_shorts(const replay_gdn_prefill_args* a)
 {
     const long long mean = (long long)a->nseq * a->nheads >= 1024 ? rs::GDN_CHUNK : 24;
